@@ -4,7 +4,8 @@ A thin ctypes layer over ``libfp8adam.so`` (C ABI in ``include/fp8adam.h``):
 the functions below carry the C names and only marshal arguments; every step
 of the optimizer runs in the library's HIP kernels.  PyTorch supplies device
 memory and the stream.  There is no fallback: if the library is missing,
-``load()`` raises.
+``load()`` raises.  The list operators (``AdamW``, ``GradClip``, ``Quantizer``;
+C ABI in ``include/fp8adam_list.h``) are in ``lists.py`` and reached from here.
 """
 from __future__ import annotations
 
@@ -490,3 +491,15 @@ class FP8AdamW:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------------ list operators
+# (at the end: the module builds on the names above)
+
+from .lists import (  # noqa: E402
+    F32, BF16, F16, LIST_EXPORTS, MAX_GROUPS, MOMENTS_8, MOMENTS_32, AdamW, AdamwConfigArg, AdamwHParamsArg,
+    AdamwTensorArg, ClipTensorArg, GradClip, QuantConfigArg, Quantizer, QuantTensorArg, fp8adam_adamw_plan,
+    fp8adam_adamw_step, fp8adam_adamw_step_amp, fp8adam_clip_grads, fp8adam_clip_plan, fp8adam_dequantize,
+    fp8adam_plan_destroy, fp8adam_quant_plan, fp8adam_quantize)
+
+EXPORTS += LIST_EXPORTS

@@ -1,8 +1,9 @@
 """Build the HIP library ``libfp8adam.so`` in-tree for gfx950 with hipcc.
 
 The step kernels are instantiated in one translation unit per (m, v) format
-pair (``csrc/fp8adam_step_*.hip``) and the C ABI is in ``csrc/fp8adam.hip``;
-the units compile in parallel, then link into one shared library.
+pair (``csrc/fp8adam_step_*.hip``) and the C ABI is in ``csrc/fp8adam.hip``,
+that of the list operators in ``csrc/fp8adam_list.hip`` (their AdamW kernels in
+``csrc/fp8adam_list_adamw*.hip``); the units compile in parallel, then link into one shared library.
 """
 from __future__ import annotations
 
@@ -16,9 +17,10 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-UNITS = [os.path.join(CSRC, "fp8adam.hip")] + sorted(glob.glob(os.path.join(CSRC, "fp8adam_step_*.hip")))
-DEPS = UNITS + [os.path.join(CSRC, "fp8_codec.h"), os.path.join(CSRC, "fp8adam_engine.h"),
-                os.path.join(ROOT, "include", "fp8adam.h")]
+UNITS = [os.path.join(CSRC, "fp8adam.hip"), os.path.join(CSRC, "fp8adam_list.hip")] + sorted(
+    glob.glob(os.path.join(CSRC, "fp8adam_step_*.hip")) + glob.glob(os.path.join(CSRC, "fp8adam_list_adamw*.hip")))
+DEPS = UNITS + [os.path.join(CSRC, h) for h in ("fp8_codec.h", "fp8adam_engine.h", "fp8adam_list.h")] + [
+    os.path.join(ROOT, "include", h) for h in ("fp8adam.h", "fp8adam_list.h")]
 LIB = os.path.join(PKG, "libfp8adam.so")
 ARCH = "gfx950"
 

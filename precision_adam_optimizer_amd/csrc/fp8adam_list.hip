@@ -1,0 +1,847 @@
+// fp8adam_list.hip -- the list operators of include/fp8adam_list.h: plans and
+// their checks, the gradient norm and clipping, the conversion to 8 bits and
+// back, and the C ABI.  The AdamW kernels are in fp8adam_list.h, instantiated
+// in fp8adam_list_adamw*.hip.
+#include <string.h>
+
+#include <algorithm>
+
+#include "fp8adam_list.h"
+
+using namespace fp8adam;
+using namespace fp8adam_engine;
+using namespace fp8adam_list;
+
+namespace fp8adam_list {
+
+extern template void launch_adamw<false, 0, 0>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
+                                               int64_t, const AdamwCtl*, hipStream_t);
+extern template void launch_adamw<true, 0, 1>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
+                                              int64_t, const AdamwCtl*, hipStream_t);
+extern template void launch_adamw<true, 0, 0>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
+                                              int64_t, const AdamwCtl*, hipStream_t);
+extern template void launch_adamw<true, 1, 0>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
+                                              int64_t, const AdamwCtl*, hipStream_t);
+extern template void launch_adamw<true, 1, 1>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
+                                              int64_t, const AdamwCtl*, hipStream_t);
+
+namespace {
+
+// ---------------------------------------------------------- norm and clipping
+//
+// The norm pass runs a fixed grid over the chunks of the list; each work-group
+// sums its chunks' squares in fp64 (a sum over 1e9 fp32 squares spans more than
+// fp32 holds; a bf16, fp16 or fp32 number's square is exact or off by 2^-53) and
+// writes one partial.  The partials are summed in one fixed order by whoever
+// needs the norm, so the result is the same in every run.  A NaN or Inf needs no
+// count of its own: no sum of finite squares overflows fp64, so the sum is not
+// finite exactly if an element is not.
+
+struct GradDesc {
+  const void* src;
+  void* dst;       // clipping only; may be null, or src
+  int64_t numel;
+  int64_t chunk0;
+  int32_t sdt, ddt;
+};
+
+constexpr int kListNormGroups = 2048;  // 8 work-groups per CU
+
+template <int DT>
+__device__ __forceinline__ void sumsq_range(const void* src, int64_t lo, int64_t hi, double& acc) {
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+    const double x = ld_elem<DT>(src, i);
+    acc = __builtin_fma(x, x, acc);
+  }
+}
+
+// Sum over the work-group's threads in a fixed order, returned to every thread.
+__device__ __forceinline__ double block_sum(double x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+  __shared__ double part[kThreads / 64];
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+  __syncthreads();
+  double s = part[0];
+#pragma unroll
+  for (int k = 1; k < kThreads / 64; k++) s += part[k];
+  return s;
+}
+
+__global__ __launch_bounds__(kThreads) void k_list_sumsq(const GradDesc* __restrict__ descs,
+                                                         const int32_t* __restrict__ chunk_tid, int64_t nchunks,
+                                                         int chunk_log2, double* __restrict__ partial) {
+  double acc = 0.0;
+  for (int64_t w = blockIdx.x; w < nchunks; w += gridDim.x) {
+    const GradDesc d = descs[chunk_tid[w]];
+    const int64_t lo = (w - d.chunk0) << chunk_log2;
+    const int64_t hi = min(lo + ((int64_t)1 << chunk_log2), d.numel);
+    if (d.sdt == FP8ADAM_F32) sumsq_range<FP8ADAM_F32>(d.src, lo, hi, acc);
+    else if (d.sdt == FP8ADAM_BF16) sumsq_range<FP8ADAM_BF16>(d.src, lo, hi, acc);
+    else sumsq_range<FP8ADAM_F16>(d.src, lo, hi, acc);
+  }
+  acc = block_sum(acc);
+  if (threadIdx.x == 0) partial[blockIdx.x] = acc;
+}
+
+// The whole sum from the partials: the same order in every work-group that asks.
+__device__ __forceinline__ double total_of(const double* __restrict__ partial, int n) {
+  double acc = 0.0;
+  for (int k = threadIdx.x; k < n; k += kThreads) acc += partial[k];
+  return block_sum(acc);
+}
+
+template <int SD, int DD>
+__device__ __forceinline__ void scale_range(const GradDesc& d, int64_t lo, int64_t hi, float coef) {
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) st_elem<DD>(d.dst, i, ld_elem<SD>(d.src, i) * coef);
+}
+
+template <int SD>
+__device__ __forceinline__ void scale_range_to(const GradDesc& d, int64_t lo, int64_t hi, float coef) {
+  if (d.ddt == FP8ADAM_F32) scale_range<SD, FP8ADAM_F32>(d, lo, hi, coef);
+  else if (d.ddt == FP8ADAM_BF16) scale_range<SD, FP8ADAM_BF16>(d, lo, hi, coef);
+  else scale_range<SD, FP8ADAM_F16>(d, lo, hi, coef);
+}
+
+__global__ __launch_bounds__(kThreads) void k_list_clip(const GradDesc* __restrict__ descs,
+                                                        const int32_t* __restrict__ chunk_tid, int64_t nchunks,
+                                                        int chunk_log2, const double* __restrict__ partial, int npartial,
+                                                        float max_norm, float* __restrict__ result) {
+  const double norm = __dsqrt_rn(total_of(partial, npartial));
+  double cc = 1.0;
+  if (max_norm > 0.0f && isfinite(norm)) {
+    cc = __ddiv_rn((double)max_norm, __dadd_rn(norm, 1e-6));
+    if (cc > 1.0) cc = 1.0;
+  }
+  const float coef = __double2float_rn(cc);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    st_global<float>(result, __double2float_rn(norm));
+    st_global<float>(result + 1, coef);
+  }
+  for (int64_t w = blockIdx.x; w < nchunks; w += gridDim.x) {
+    const GradDesc d = descs[chunk_tid[w]];
+    if (d.dst == nullptr || (coef == 1.0f && d.dst == d.src)) continue;  // uniform: nothing to write, or nothing changes
+    const int64_t lo = (w - d.chunk0) << chunk_log2;
+    const int64_t hi = min(lo + ((int64_t)1 << chunk_log2), d.numel);
+    if (d.sdt == FP8ADAM_F32) scale_range_to<FP8ADAM_F32>(d, lo, hi, coef);
+    else if (d.sdt == FP8ADAM_BF16) scale_range_to<FP8ADAM_BF16>(d, lo, hi, coef);
+    else scale_range_to<FP8ADAM_F16>(d, lo, hi, coef);
+  }
+}
+
+// Loss scaling: the scaler's decision, and each group's bias corrections at the
+// device-side t.
+struct GroupRates {
+  double lr[FP8ADAM_MAX_GROUPS], beta1[FP8ADAM_MAX_GROUPS], beta2[FP8ADAM_MAX_GROUPS];
+};
+
+__global__ __launch_bounds__(kThreads) void k_list_ctl(const double* __restrict__ partial, int npartial,
+                                                       fp8adam_amp_state* __restrict__ st, AdamwCtl* __restrict__ ctl,
+                                                       fp8adam_amp_config cfg, GroupRates R, int n_groups) {
+  const double sumsq = total_of(partial, npartial);
+  __shared__ int64_t t_now;
+  if (threadIdx.x == 0) {
+    float gfac = 0.0f;
+    int64_t t = 0;
+    const bool run = scaler_decide(st, cfg, sumsq, !isfinite(sumsq), gfac, t);
+    ctl->skip = run ? 0 : 1;
+    ctl->gfac = gfac;
+    t_now = t;
+  }
+  __syncthreads();
+  const int q = threadIdx.x;
+  if (q < n_groups && t_now > 0) {
+    ctl->step_size[q] = (float)(R.lr[q] / (1.0 - pow(R.beta1[q], (double)t_now)));
+    ctl->inv_bc2[q] = (float)(1.0 / (1.0 - pow(R.beta2[q], (double)t_now)));
+  }
+}
+
+// -------------------------------------------------------- conversion to 8 bits
+
+struct QuantDesc {
+  void* x;
+  uint8_t* codes;
+  float* scale;
+  int64_t numel;
+  int64_t part0;
+  int64_t chunk0;    // per-tensor scales: its first amax chunk, their number and length
+  int64_t nchunks;
+  int64_t chunk_len;
+};
+
+constexpr int kQuantPartLog2 = 10;        // elements of a block-scaled or dequantizing work-group
+constexpr int kQuantTensorPartLog2 = 13;  // of one that quantizes with a tensor's scale
+constexpr int64_t kAmaxMaxChunks = 512;   // amax chunks per tensor at most (each quantizing work-group reads them all)
+constexpr int64_t kAmaxMinChunk = 8192;
+
+template <int FMT>
+__device__ __forceinline__ void choose_scale_mode(uint32_t amax, int smode, float& s, float& inv) {
+  if (smode == FP8ADAM_SCALE_POW2) choose_scale<FMT, 0>(amax, s, inv);
+  else choose_scale<FMT, 1>(amax, s, inv);
+}
+
+// One work-group per part, 32 lanes per block of 128 (lane h: its elements h,
+// h + 32, h + 64, h + 96).
+template <int DT, int FMT>
+__global__ __launch_bounds__(kThreads) void k_quant_block(const QuantDesc* __restrict__ descs,
+                                                          const int32_t* __restrict__ part_tid, int64_t nparts,
+                                                          int smode) {
+  const int64_t w = work_index<kXcdStreams>(nparts);
+  if (w < 0) return;
+  const QuantDesc d = descs[part_tid[w]];
+  const int64_t block = ((w - d.part0) << (kQuantPartLog2 - 7)) + (threadIdx.x >> 5);
+  const int64_t i0 = block * kBlock + (threadIdx.x & 31);
+  float x[4];
+  uint32_t am = 0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    x[j] = i0 + 32 * j < d.numel ? ld_elem<DT>(d.x, i0 + 32 * j) : 0.0f;
+    am = max(am, abs_bits(x[j]));
+  }
+  float s, inv;
+  am = group32_max(am);
+  choose_scale_mode<FMT>(am, smode, s, inv);
+  if (block * kBlock < d.numel && (threadIdx.x & 31) == 0) st_global<float>(d.scale + block, s);
+#pragma unroll
+  for (int j = 0; j < 4; j++) x[j] *= inv;
+  const uint32_t codes = encode4_nan<FMT>(x, nonfinite_amax(am));
+#pragma unroll
+  for (int j = 0; j < 4; j++)
+    if (i0 + 32 * j < d.numel) st_global<uint8_t>(d.codes + i0 + 32 * j, (uint8_t)(codes >> (8 * j)));
+}
+
+// Per-tensor scales, first pass: the amax of one chunk.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_quant_amax(const QuantDesc* __restrict__ descs,
+                                                         const int32_t* __restrict__ chunk_tid,
+                                                         uint32_t* __restrict__ amax) {
+  const int64_t w = blockIdx.x;
+  const QuantDesc d = descs[chunk_tid[w]];
+  const int64_t lo = (w - d.chunk0) * d.chunk_len, hi = min(lo + d.chunk_len, d.numel);
+  uint32_t am = 0, none = 0;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) am = max(am, abs_bits(ld_elem<DT>(d.x, i)));
+  block_max2(am, none);
+  if (threadIdx.x == 0) amax[w] = am;
+}
+
+// Second pass: every work-group takes the largest of its tensor's chunk maxima
+// (at most kAmaxMaxChunks of them, from the L2), and quantizes its part.
+template <int DT, int FMT>
+__global__ __launch_bounds__(kThreads) void k_quant_tensor(const QuantDesc* __restrict__ descs,
+                                                           const int32_t* __restrict__ part_tid, int64_t nparts,
+                                                           const uint32_t* __restrict__ amax, int smode) {
+  const int64_t w = work_index<kXcdStreams>(nparts);
+  if (w < 0) return;
+  const QuantDesc d = descs[part_tid[w]];
+  uint32_t am = 0;
+  for (int64_t k = threadIdx.x & 63; k < d.nchunks; k += 64) am = max(am, amax[d.chunk0 + k]);
+  float s, inv;
+  am = wave_max(am);
+  choose_scale_mode<FMT>(am, smode, s, inv);
+  if (w == d.part0 && threadIdx.x == 0) st_global<float>(d.scale, s);
+  const int64_t lo = (w - d.part0) << kQuantTensorPartLog2;
+  const int64_t hi = min(lo + ((int64_t)1 << kQuantTensorPartLog2), d.numel);
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+    const float x[4] = {ld_elem<DT>(d.x, i) * inv, 0.0f, 0.0f, 0.0f};
+    st_global<uint8_t>(d.codes + i, (uint8_t)encode4_nan<FMT>(x, nonfinite_amax(am)));
+  }
+}
+
+template <int DT, int FMT, bool BLK>
+__global__ __launch_bounds__(kThreads) void k_dequant(const QuantDesc* __restrict__ descs,
+                                                      const int32_t* __restrict__ part_tid, int64_t nparts,
+                                                      int part_log2) {
+  const int64_t w = work_index<kXcdStreams>(nparts);
+  if (w < 0) return;
+  const QuantDesc d = descs[part_tid[w]];
+  const int64_t lo = (w - d.part0) << part_log2;
+  const int64_t hi = min(lo + ((int64_t)1 << part_log2), d.numel);
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads)
+    st_elem<DT>(d.x, i, decode1<FMT>(ld_global<uint8_t>(d.codes + i)) * ld_global<float>(d.scale + (BLK ? i >> 7 : 0)));
+}
+
+// ------------------------------------------------------------------- host side
+
+enum PlanKind { kPlanAdamw = 0, kPlanClip = 1, kPlanQuant = 2 };
+
+// The parts of one kind of tensor.
+struct Span {
+  AdamwKind kind{};          // AdamW
+  int dtype = 0, format = 0; // conversion
+  std::vector<int32_t> tid;  // part -> tensor (host copy, until it is uploaded)
+  const int32_t* d_tid = nullptr;
+  int64_t nparts = 0;
+  std::vector<int32_t> ctid; // amax chunk -> tensor
+  const int32_t* d_ctid = nullptr;
+  int64_t nchunks = 0;
+  int64_t chunk_base = 0;    // the kind's first amax chunk in the plan's array
+};
+
+bool valid_dtype(int32_t d) { return d >= FP8ADAM_F32 && d <= FP8ADAM_F16; }
+bool valid_format(int32_t f) { return f == FP8ADAM_E4M3 || f == FP8ADAM_E5M2; }
+
+// Elements of one plan: every launch has to fit one grid dimension (2^32 - 1
+// work-items of work-groups of 1024 elements).
+constexpr int64_t kMaxGroupsPerLaunch = ((int64_t)UINT32_MAX / kThreads) & ~(int64_t)7;
+
+std::string of_tensor(const char* what, int32_t t) { return std::string(what) + " of tensor " + std::to_string(t); }
+
+// The memory ranges of a list: what a call writes may not overlap anything else.
+struct Range {
+  uintptr_t lo, hi;
+  bool written;
+  int32_t tensor;
+};
+
+struct Ranges {
+  std::vector<Range> all;
+  // One tensor of n elements of `bytes` each: null and alignment are checked too.
+  int add(const void* p, int64_t n, int64_t bytes, bool written, const char* what, int32_t t) {
+    if (!p) return fail(FP8ADAM_EINVAL, of_tensor(what, t) + " is null");
+    const uintptr_t a = (uintptr_t)p;
+    if (a % (uintptr_t)bytes)
+      return fail(FP8ADAM_EALIGN, of_tensor(what, t) + " is not aligned to its element size (" + std::to_string(bytes) + ")");
+    all.push_back(Range{a, a + (uintptr_t)(n * bytes), written, t});
+    return 0;
+  }
+  int check() {
+    std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    const Range *any = nullptr, *written = nullptr;  // the earlier ranges that reach furthest
+    for (const Range& r : all) {
+      const Range* hit = written && r.lo < written->hi ? written : r.written && any && r.lo < any->hi ? any : nullptr;
+      if (hit)
+        return fail(FP8ADAM_EINVAL, "memory that the call writes overlaps other memory of the list (tensors " +
+                                        std::to_string(hit->tensor) + " and " + std::to_string(r.tensor) + ")");
+      if (!any || r.hi > any->hi) any = &r;
+      if (r.written && (!written || r.hi > written->hi)) written = &r;
+    }
+    return 0;
+  }
+};
+
+int check_numel(int64_t numel, int64_t& total, int32_t t) {
+  if (numel < 0) return fail(FP8ADAM_EINVAL, of_tensor("numel", t) + " is negative");
+  constexpr int64_t most = kMaxGroupsPerLaunch << 10;
+  if (numel > most || (total += numel) > most)
+    return fail(FP8ADAM_EINVAL, "too many elements for one plan (at most " + std::to_string(most) +
+                                    "); split the list over several plans");
+  return 0;
+}
+
+int check_parts(int64_t parts) {
+  if (parts > kMaxGroupsPerLaunch)
+    return fail(FP8ADAM_EINVAL, "too many elements for one plan once each tensor is rounded up to whole parts");
+  return 0;
+}
+
+}  // namespace
+}  // namespace fp8adam_list
+
+struct fp8adam_plan {
+  PlanKind kind = kPlanAdamw;
+  int device = 0;
+  int mf = 0, vf = 0, n_groups = 1;       // AdamW
+  int granularity = 0, smode = 0;         // conversion
+  std::vector<Span> spans;
+  unsigned char* mem = nullptr;           // one allocation: descriptors, tables, workspace
+  const void* d_desc = nullptr;
+  // the gradient list (AdamW and clipping)
+  const GradDesc* d_grad = nullptr;
+  const int32_t* d_grad_tid = nullptr;
+  int64_t grad_chunks = 0;
+  int grad_chunk_log2 = 0;
+  double* d_partial = nullptr;
+  AdamwCtl* d_ctl = nullptr;
+  uint32_t* d_amax = nullptr;             // conversion with per-tensor scales: one per chunk
+  int norm_groups() const { return (int)std::min<int64_t>(grad_chunks, kListNormGroups); }
+  ~fp8adam_plan() {
+    if (mem) (void)hipFree(mem);
+  }
+};
+
+namespace fp8adam_list {
+namespace {
+
+// The device image of a plan: pieces at 256-byte offsets of one allocation.
+struct Image {
+  std::vector<unsigned char> bytes;  // what is uploaded
+  size_t size = 0;                   // and the workspace behind it
+  size_t put(const void* p, size_t n) {
+    const size_t at = bytes.size();
+    bytes.resize((at + n + 255) & ~(size_t)255);
+    if (n) memcpy(bytes.data() + at, p, n);
+    size = bytes.size();
+    return at;
+  }
+  size_t room(size_t n) {  // after every put
+    const size_t at = size;
+    size = (size + n + 255) & ~(size_t)255;
+    return at;
+  }
+  int upload(fp8adam_plan* p, hipStream_t stream) {
+    hipError_t e = hipMalloc((void**)&p->mem, std::max<size_t>(size, 256));
+    if (e == hipErrorOutOfMemory) return fail(FP8ADAM_ENOMEM, "device allocation failed");
+    if (e == hipSuccess && !bytes.empty())
+      e = hipMemcpyAsync(p->mem, bytes.data(), bytes.size(), hipMemcpyHostToDevice, stream);
+    if (e == hipSuccess) e = hipStreamSynchronize(stream);
+    return e == hipSuccess ? 0 : hip_fail(e, "uploading the plan");
+  }
+};
+
+// The current device, which the stream has to belong to.
+int plan_device(fp8adam_plan* p, hipStream_t stream) {
+  HIP_TRY(hipGetDevice(&p->device));
+  hipDevice_t dev = -1;
+  HIP_TRY(hipStreamGetDevice(stream, &dev));
+  if (dev != p->device)
+    return fail(FP8ADAM_EINVAL, "the stream belongs to device " + std::to_string(dev) + ", not the current device " +
+                                    std::to_string(p->device));
+  return 0;
+}
+
+int check_call(const fp8adam_plan* p, PlanKind kind, const char* what, hipStream_t stream) {
+  if (!p) return fail(FP8ADAM_EINVAL, "plan is null");
+  if (p->kind != kind) return fail(FP8ADAM_EINVAL, std::string("the plan is not one of ") + what);
+  hipDevice_t dev = -1;
+  HIP_TRY(hipStreamGetDevice(stream, &dev));
+  if (dev != p->device)
+    return fail(FP8ADAM_EINVAL, "the stream belongs to device " + std::to_string(dev) + ", the plan to device " +
+                                    std::to_string(p->device));
+  return 0;
+}
+
+// Chunks of the gradient list: the largest power of two of 4096 .. 32768
+// elements that still gives the norm pass a work-group for each of its places.
+void chunk_grads(std::vector<GradDesc>& g, int64_t total, int& chunk_log2, std::vector<int32_t>& tid) {
+  chunk_log2 = 15;
+  while (chunk_log2 > 12 && (total >> chunk_log2) < kListNormGroups) chunk_log2--;
+  for (size_t t = 0; t < g.size(); t++) {
+    g[t].chunk0 = (int64_t)tid.size();
+    const int64_t nc = (g[t].numel + ((int64_t)1 << chunk_log2) - 1) >> chunk_log2;
+    tid.insert(tid.end(), (size_t)nc, (int32_t)t);
+  }
+}
+
+void launch_sumsq(const fp8adam_plan* p, hipStream_t s) {
+  if (p->grad_chunks)
+    hipLaunchKernelGGL(k_list_sumsq, dim3((unsigned)p->norm_groups()), dim3(kThreads), 0, s, p->d_grad, p->d_grad_tid,
+                       p->grad_chunks, p->grad_chunk_log2, p->d_partial);
+}
+
+int run_adamw(fp8adam_plan* p, const AdamwConsts& C, const AdamwCtl* ctl, hipStream_t s) {
+  const AdamwDesc* d = static_cast<const AdamwDesc*>(p->d_desc);
+  for (const Span& k : p->spans) {
+    if (!k.kind.moments8) launch_adamw<false, 0, 0>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
+    else if (p->mf == 0 && p->vf == 1) launch_adamw<true, 0, 1>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
+    else if (p->mf == 0) launch_adamw<true, 0, 0>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
+    else if (p->vf == 0) launch_adamw<true, 1, 0>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
+    else launch_adamw<true, 1, 1>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
+    HIP_TRY(hipGetLastError());
+  }
+  return 0;
+}
+
+int check_groups(const fp8adam_plan* p, const fp8adam_adamw_hparams* h, int32_t n_groups) {
+  if (!h) return fail(FP8ADAM_EINVAL, "groups is null");
+  if (n_groups != p->n_groups)
+    return fail(FP8ADAM_EINVAL, "n_groups is " + std::to_string(n_groups) + ", the plan has " + std::to_string(p->n_groups));
+  for (int q = 0; q < n_groups; q++) {
+    if (!(h[q].beta1 >= 0.0 && h[q].beta1 < 1.0) || !(h[q].beta2 >= 0.0 && h[q].beta2 < 1.0))
+      return fail(FP8ADAM_EINVAL, "beta1 and beta2 must lie in [0, 1)");
+    if (!(h[q].eps >= 0.0) || !isfinite(h[q].eps)) return fail(FP8ADAM_EINVAL, "eps must be finite and >= 0");
+    if (!isfinite(h[q].lr) || !isfinite(h[q].weight_decay))
+      return fail(FP8ADAM_EINVAL, "lr and weight_decay must be finite");
+  }
+  return 0;
+}
+
+// t < 1: the bias corrections come from the device.
+void group_consts(const fp8adam_adamw_hparams* h, int n_groups, int64_t t, AdamwConsts& C) {
+  for (int q = 0; q < n_groups; q++) {
+    GroupConsts& c = C.g[q];
+    c.b1 = (float)h[q].beta1;
+    c.omb1 = (float)(1.0 - h[q].beta1);
+    c.b2 = (float)h[q].beta2;
+    c.omb2 = (float)(1.0 - h[q].beta2);
+    c.lr_wd = (float)(h[q].lr * h[q].weight_decay);
+    c.eps = (float)h[q].eps;
+    c.step_size = t < 1 ? 0.0f : (float)(h[q].lr / (1.0 - pow(h[q].beta1, (double)t)));
+    c.inv_bc2 = t < 1 ? 0.0f : (float)(1.0 / (1.0 - pow(h[q].beta2, (double)t)));
+  }
+}
+
+template <int DT, int FMT>
+int run_quantize(fp8adam_plan* p, const Span& k, hipStream_t s) {
+  const QuantDesc* d = static_cast<const QuantDesc*>(p->d_desc);
+  const dim3 grid(grid_for<kXcdStreams>(k.nparts));
+  if (p->granularity == FP8ADAM_SCALE_BLOCK128) {
+    hipLaunchKernelGGL((k_quant_block<DT, FMT>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts, p->smode);
+  } else {
+    uint32_t* amax = p->d_amax + k.chunk_base;
+    hipLaunchKernelGGL((k_quant_amax<DT>), dim3((unsigned)k.nchunks), dim3(kThreads), 0, s, d, k.d_ctid, amax);
+    HIP_TRY(hipGetLastError());
+    hipLaunchKernelGGL((k_quant_tensor<DT, FMT>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts, amax, p->smode);
+  }
+  HIP_TRY(hipGetLastError());
+  return 0;
+}
+
+template <int DT, int FMT>
+int run_dequantize(fp8adam_plan* p, const Span& k, hipStream_t s) {
+  const QuantDesc* d = static_cast<const QuantDesc*>(p->d_desc);
+  const dim3 grid(grid_for<kXcdStreams>(k.nparts));
+  if (p->granularity == FP8ADAM_SCALE_BLOCK128)
+    hipLaunchKernelGGL((k_dequant<DT, FMT, true>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts, kQuantPartLog2);
+  else
+    hipLaunchKernelGGL((k_dequant<DT, FMT, false>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts,
+                       kQuantTensorPartLog2);
+  HIP_TRY(hipGetLastError());
+  return 0;
+}
+
+template <int FMT>
+int run_convert(fp8adam_plan* p, const Span& k, bool back, hipStream_t s) {
+  if (k.dtype == FP8ADAM_F32)
+    return back ? run_dequantize<FP8ADAM_F32, FMT>(p, k, s) : run_quantize<FP8ADAM_F32, FMT>(p, k, s);
+  if (k.dtype == FP8ADAM_BF16)
+    return back ? run_dequantize<FP8ADAM_BF16, FMT>(p, k, s) : run_quantize<FP8ADAM_BF16, FMT>(p, k, s);
+  return back ? run_dequantize<FP8ADAM_F16, FMT>(p, k, s) : run_quantize<FP8ADAM_F16, FMT>(p, k, s);
+}
+
+int convert(fp8adam_plan* p, bool back, hipStream_t stream) {
+  if (int r = check_call(p, kPlanQuant, "fp8adam_quant_plan", stream)) return r;
+  for (const Span& k : p->spans)
+    if (int r = k.format == FP8ADAM_E4M3 ? run_convert<0>(p, k, back, stream) : run_convert<1>(p, k, back, stream))
+      return r;
+  return 0;
+}
+
+// A new plan, freed unless it is handed out.
+struct NewPlan {
+  fp8adam_plan* p = new fp8adam_plan();
+  ~NewPlan() { delete p; }
+  fp8adam_plan* release() {
+    fp8adam_plan* q = p;
+    p = nullptr;
+    return q;
+  }
+};
+
+int adamw_plan(fp8adam_plan** out, const fp8adam_adamw_tensor* T, int32_t n, const fp8adam_adamw_config* cfg,
+               hipStream_t stream) {
+  if (!T || !cfg) return fail(FP8ADAM_EINVAL, "tensors or cfg is null");
+  if (n <= 0) return fail(FP8ADAM_EINVAL, "n must be positive");
+  if (!valid_format(cfg->m_format) || !valid_format(cfg->v_format))
+    return fail(FP8ADAM_EINVAL, "m_format / v_format must be FP8ADAM_E4M3 or FP8ADAM_E5M2");
+  if (cfg->n_groups < 1 || cfg->n_groups > FP8ADAM_MAX_GROUPS)
+    return fail(FP8ADAM_EINVAL, "n_groups must lie in [1, " + std::to_string(FP8ADAM_MAX_GROUPS) + "]");
+  int64_t total = 0;
+  Ranges ranges;
+  for (int32_t t = 0; t < n; t++) {
+    const fp8adam_adamw_tensor& x = T[t];
+    if (int r = check_numel(x.numel, total, t)) return r;
+    if (!valid_dtype(x.param_dtype) || !valid_dtype(x.grad_dtype)) return fail(FP8ADAM_EINVAL, of_tensor("bad dtype", t));
+    if (x.copy && (x.param_dtype != FP8ADAM_F32 || (x.copy_dtype != FP8ADAM_BF16 && x.copy_dtype != FP8ADAM_F16)))
+      return fail(FP8ADAM_EINVAL, of_tensor("copy", t) + " must be bf16 or fp16, and its weights fp32");
+    if (x.moments != FP8ADAM_MOMENTS_32 && x.moments != FP8ADAM_MOMENTS_8)
+      return fail(FP8ADAM_EINVAL, of_tensor("bad moments", t));
+    if (x.group < 0 || x.group >= cfg->n_groups) return fail(FP8ADAM_EINVAL, of_tensor("group", t) + " is out of range");
+    if (x.numel == 0) continue;
+    const bool s8 = x.moments == FP8ADAM_MOMENTS_8;
+    if (int r = ranges.add(x.param, x.numel, dtype_bytes(x.param_dtype), true, "param", t)) return r;
+    if (int r = ranges.add(x.grad, x.numel, dtype_bytes(x.grad_dtype), false, "grad", t)) return r;
+    if (int r = ranges.add(x.m, x.numel, s8 ? 1 : 4, true, "m", t)) return r;
+    if (int r = ranges.add(x.v, x.numel, s8 ? 1 : 4, true, "v", t)) return r;
+    if (x.copy)
+      if (int r = ranges.add(x.copy, x.numel, 2, true, "copy", t)) return r;
+    if (s8) {
+      const int64_t ns = (x.numel + kBlock - 1) / kBlock;
+      if (int r = ranges.add(x.m_scale, ns, 4, true, "m_scale", t)) return r;
+      if (int r = ranges.add(x.v_scale, ns, 4, true, "v_scale", t)) return r;
+    }
+  }
+  if (int r = ranges.check()) return r;
+
+  NewPlan np;
+  fp8adam_plan* p = np.p;
+  p->kind = kPlanAdamw;
+  p->mf = cfg->m_format;
+  p->vf = cfg->v_format;
+  p->n_groups = cfg->n_groups;
+  std::vector<AdamwDesc> desc((size_t)n);
+  std::vector<GradDesc> grads((size_t)n);
+  for (int32_t t = 0; t < n; t++) {
+    const fp8adam_adamw_tensor& x = T[t];
+    grads[t] = GradDesc{x.grad, nullptr, x.numel, 0, x.grad_dtype, 0};
+    desc[t] = AdamwDesc{x.param, x.grad, x.copy, x.m, x.v, x.m_scale, x.v_scale, x.numel, 0, x.group, 0};
+    if (x.numel == 0) continue;
+    const AdamwKind kind{x.param_dtype, x.copy ? x.copy_dtype : 0, x.grad_dtype, x.moments == FP8ADAM_MOMENTS_8};
+    auto it = std::find_if(p->spans.begin(), p->spans.end(), [&](const Span& k) { return k.kind == kind; });
+    if (it == p->spans.end()) {
+      p->spans.emplace_back();
+      it = p->spans.end() - 1;
+      it->kind = kind;
+    }
+    desc[t].part0 = (int64_t)it->tid.size();
+    const int64_t parts = (x.numel + ((int64_t)1 << kAdamwPartLog2) - 1) >> kAdamwPartLog2;
+    if (int r = check_parts(desc[t].part0 + parts)) return r;
+    it->tid.insert(it->tid.end(), (size_t)parts, t);
+  }
+  std::vector<int32_t> gtid;
+  chunk_grads(grads, total, p->grad_chunk_log2, gtid);
+  p->grad_chunks = (int64_t)gtid.size();
+  if (int r = plan_device(p, stream)) return r;
+  Image im;
+  const size_t at_desc = im.put(desc.data(), sizeof(AdamwDesc) * desc.size());
+  const size_t at_grad = im.put(grads.data(), sizeof(GradDesc) * grads.size());
+  const size_t at_gtid = im.put(gtid.data(), sizeof(int32_t) * gtid.size());
+  std::vector<size_t> at;
+  for (Span& k : p->spans) at.push_back(im.put(k.tid.data(), sizeof(int32_t) * k.tid.size()));
+  const size_t at_partial = im.room(sizeof(double) * kListNormGroups), at_ctl = im.room(sizeof(AdamwCtl));
+  if (int r = im.upload(p, stream)) return r;
+  p->d_desc = p->mem + at_desc;
+  p->d_grad = reinterpret_cast<const GradDesc*>(p->mem + at_grad);
+  p->d_grad_tid = reinterpret_cast<const int32_t*>(p->mem + at_gtid);
+  p->d_partial = reinterpret_cast<double*>(p->mem + at_partial);
+  p->d_ctl = reinterpret_cast<AdamwCtl*>(p->mem + at_ctl);
+  for (size_t k = 0; k < at.size(); k++) {
+    p->spans[k].d_tid = reinterpret_cast<const int32_t*>(p->mem + at[k]);
+    p->spans[k].nparts = (int64_t)p->spans[k].tid.size();
+    std::vector<int32_t>().swap(p->spans[k].tid);
+  }
+  *out = np.release();
+  return 0;
+}
+
+int clip_plan(fp8adam_plan** out, const fp8adam_clip_tensor* T, int32_t n, hipStream_t stream) {
+  if (!T) return fail(FP8ADAM_EINVAL, "tensors is null");
+  if (n <= 0) return fail(FP8ADAM_EINVAL, "n must be positive");
+  int64_t total = 0;
+  Ranges ranges;
+  for (int32_t t = 0; t < n; t++) {
+    const fp8adam_clip_tensor& x = T[t];
+    if (int r = check_numel(x.numel, total, t)) return r;
+    if (!valid_dtype(x.src_dtype) || (x.dst && !valid_dtype(x.dst_dtype)))
+      return fail(FP8ADAM_EINVAL, of_tensor("bad dtype", t));
+    if (x.numel == 0) continue;
+    const bool in_place = x.dst == x.src;
+    if (in_place && x.dst && x.dst_dtype != x.src_dtype)
+      return fail(FP8ADAM_EINVAL, of_tensor("dst", t) + " is src itself, so it must have its type");
+    if (int r = ranges.add(x.src, x.numel, dtype_bytes(x.src_dtype), in_place, "src", t)) return r;
+    if (x.dst && !in_place)
+      if (int r = ranges.add(x.dst, x.numel, dtype_bytes(x.dst_dtype), true, "dst", t)) return r;
+  }
+  if (int r = ranges.check()) return r;
+  NewPlan np;
+  fp8adam_plan* p = np.p;
+  p->kind = kPlanClip;
+  std::vector<GradDesc> grads((size_t)n);
+  for (int32_t t = 0; t < n; t++)
+    grads[t] = GradDesc{T[t].src, T[t].dst, T[t].numel, 0, T[t].src_dtype, T[t].dst_dtype};
+  std::vector<int32_t> gtid;
+  chunk_grads(grads, total, p->grad_chunk_log2, gtid);
+  p->grad_chunks = (int64_t)gtid.size();
+  if (int r = plan_device(p, stream)) return r;
+  Image im;
+  const size_t at_grad = im.put(grads.data(), sizeof(GradDesc) * grads.size());
+  const size_t at_gtid = im.put(gtid.data(), sizeof(int32_t) * gtid.size());
+  const size_t at_partial = im.room(sizeof(double) * kListNormGroups);
+  if (int r = im.upload(p, stream)) return r;
+  p->d_grad = reinterpret_cast<const GradDesc*>(p->mem + at_grad);
+  p->d_grad_tid = reinterpret_cast<const int32_t*>(p->mem + at_gtid);
+  p->d_partial = reinterpret_cast<double*>(p->mem + at_partial);
+  *out = np.release();
+  return 0;
+}
+
+int quant_plan(fp8adam_plan** out, const fp8adam_quant_tensor* T, int32_t n, const fp8adam_quant_config* cfg,
+               hipStream_t stream) {
+  if (!T || !cfg) return fail(FP8ADAM_EINVAL, "tensors or cfg is null");
+  if (n <= 0) return fail(FP8ADAM_EINVAL, "n must be positive");
+  if (cfg->granularity != FP8ADAM_SCALE_TENSOR && cfg->granularity != FP8ADAM_SCALE_BLOCK128)
+    return fail(FP8ADAM_EINVAL, "bad granularity");
+  if (cfg->scale_mode != FP8ADAM_SCALE_POW2 && cfg->scale_mode != FP8ADAM_SCALE_AMAX)
+    return fail(FP8ADAM_EINVAL, "bad scale_mode");
+  const bool block = cfg->granularity == FP8ADAM_SCALE_BLOCK128;
+  int64_t total = 0;
+  Ranges ranges;
+  for (int32_t t = 0; t < n; t++) {
+    const fp8adam_quant_tensor& x = T[t];
+    if (int r = check_numel(x.numel, total, t)) return r;
+    if (!valid_dtype(x.dtype)) return fail(FP8ADAM_EINVAL, of_tensor("bad dtype", t));
+    if (!valid_format(x.format)) return fail(FP8ADAM_EINVAL, of_tensor("bad format", t));
+    if (x.numel == 0) continue;
+    if (int r = ranges.add(x.values, x.numel, dtype_bytes(x.dtype), true, "values", t)) return r;
+    if (int r = ranges.add(x.codes, x.numel, 1, true, "codes", t)) return r;
+    if (int r = ranges.add(x.scale, block ? (x.numel + kBlock - 1) / kBlock : 1, 4, true, "scale", t)) return r;
+  }
+  if (int r = ranges.check()) return r;
+  NewPlan np;
+  fp8adam_plan* p = np.p;
+  p->kind = kPlanQuant;
+  p->granularity = cfg->granularity;
+  p->smode = cfg->scale_mode;
+  const int pl = block ? kQuantPartLog2 : kQuantTensorPartLog2;
+  std::vector<QuantDesc> desc((size_t)n);
+  for (int32_t t = 0; t < n; t++) {
+    const fp8adam_quant_tensor& x = T[t];
+    QuantDesc& d = desc[t];
+    d = QuantDesc{x.values, x.codes, x.scale, x.numel, 0, 0, 0, 0};
+    if (x.numel == 0) continue;
+    auto it = std::find_if(p->spans.begin(), p->spans.end(),
+                           [&](const Span& k) { return k.dtype == x.dtype && k.format == x.format; });
+    if (it == p->spans.end()) {
+      p->spans.emplace_back();
+      it = p->spans.end() - 1;
+      it->dtype = x.dtype;
+      it->format = x.format;
+    }
+    d.part0 = (int64_t)it->tid.size();
+    const int64_t parts = (x.numel + ((int64_t)1 << pl) - 1) >> pl;
+    if (int r = check_parts(d.part0 + parts)) return r;
+    it->tid.insert(it->tid.end(), (size_t)parts, t);
+    if (!block) {
+      d.chunk0 = (int64_t)it->ctid.size();
+      const int64_t len = (x.numel + kAmaxMaxChunks - 1) / kAmaxMaxChunks;
+      d.chunk_len = (len + kAmaxMinChunk - 1) / kAmaxMinChunk * kAmaxMinChunk;
+      d.nchunks = (x.numel + d.chunk_len - 1) / d.chunk_len;
+      it->ctid.insert(it->ctid.end(), (size_t)d.nchunks, t);
+    }
+  }
+  if (int r = plan_device(p, stream)) return r;
+  Image im;
+  const size_t at_desc = im.put(desc.data(), sizeof(QuantDesc) * desc.size());
+  std::vector<size_t> at, atc;
+  int64_t chunks = 0;
+  for (Span& k : p->spans) {
+    at.push_back(im.put(k.tid.data(), sizeof(int32_t) * k.tid.size()));
+    atc.push_back(im.put(k.ctid.data(), sizeof(int32_t) * k.ctid.size()));
+    k.chunk_base = chunks;
+    chunks += (int64_t)k.ctid.size();
+  }
+  const size_t at_amax = im.room(sizeof(uint32_t) * (size_t)chunks);
+  if (int r = im.upload(p, stream)) return r;
+  p->d_desc = p->mem + at_desc;
+  p->d_amax = reinterpret_cast<uint32_t*>(p->mem + at_amax);
+  for (size_t k = 0; k < at.size(); k++) {
+    Span& s = p->spans[k];
+    s.d_tid = reinterpret_cast<const int32_t*>(p->mem + at[k]);
+    s.d_ctid = reinterpret_cast<const int32_t*>(p->mem + atc[k]);
+    s.nparts = (int64_t)s.tid.size();
+    s.nchunks = (int64_t)s.ctid.size();
+    std::vector<int32_t>().swap(s.tid);
+    std::vector<int32_t>().swap(s.ctid);
+  }
+  *out = np.release();
+  return 0;
+}
+
+// Nothing is thrown across the ABI: every entry point runs its body in here.
+template <typename F>
+int guarded(const char* what, F&& body) {
+  try {
+    return body();
+  } catch (const std::bad_alloc&) {
+    return fail(FP8ADAM_ENOMEM, "host allocation failed");
+  } catch (...) {
+    return fail(FP8ADAM_EINVAL, std::string("unexpected error in ") + what);
+  }
+}
+
+template <typename F>
+int guarded_plan(fp8adam_plan** out, const char* what, F&& body) {
+  return guarded(what, [&]() -> int {
+    if (!out) return fail(FP8ADAM_EINVAL, "out is null");
+    *out = nullptr;
+    return body();
+  });
+}
+
+}  // namespace
+}  // namespace fp8adam_list
+
+// ================================================================== C ABI
+
+extern "C" {
+
+void fp8adam_plan_destroy(fp8adam_plan* plan) { delete plan; }
+
+int fp8adam_adamw_plan(fp8adam_plan** out, const fp8adam_adamw_tensor* tensors, int32_t n,
+                       const fp8adam_adamw_config* cfg, hipStream_t stream) {
+  return guarded_plan(out, "fp8adam_adamw_plan", [&] { return adamw_plan(out, tensors, n, cfg, stream); });
+}
+
+int fp8adam_clip_plan(fp8adam_plan** out, const fp8adam_clip_tensor* tensors, int32_t n, hipStream_t stream) {
+  return guarded_plan(out, "fp8adam_clip_plan", [&] { return clip_plan(out, tensors, n, stream); });
+}
+
+int fp8adam_quant_plan(fp8adam_plan** out, const fp8adam_quant_tensor* tensors, int32_t n,
+                       const fp8adam_quant_config* cfg, hipStream_t stream) {
+  return guarded_plan(out, "fp8adam_quant_plan", [&] { return quant_plan(out, tensors, n, cfg, stream); });
+}
+
+int fp8adam_adamw_step(fp8adam_plan* plan, const fp8adam_adamw_hparams* groups, int32_t n_groups, int64_t step,
+                       hipStream_t stream) {
+  return guarded("fp8adam_adamw_step", [&]() -> int {
+    if (int r = check_call(plan, kPlanAdamw, "fp8adam_adamw_plan", stream)) return r;
+    if (int r = check_groups(plan, groups, n_groups)) return r;
+    if (step < 1) return fail(FP8ADAM_EINVAL, "step must be >= 1");
+    AdamwConsts C{};
+    group_consts(groups, n_groups, step, C);
+    return run_adamw(plan, C, nullptr, stream);
+  });
+}
+
+int fp8adam_adamw_step_amp(fp8adam_plan* plan, const fp8adam_adamw_hparams* groups, int32_t n_groups,
+                           const fp8adam_amp_config* amp, fp8adam_amp_state* state, hipStream_t stream) {
+  return guarded("fp8adam_adamw_step_amp", [&]() -> int {
+    if (int r = check_call(plan, kPlanAdamw, "fp8adam_adamw_plan", stream)) return r;
+    if (int r = check_groups(plan, groups, n_groups)) return r;
+    if (!amp || !state) return fail(FP8ADAM_EINVAL, "amp or state is null");
+    if ((uintptr_t)state & 7u) return fail(FP8ADAM_EINVAL, "state must be 8-byte aligned");
+    if (!(amp->growth_factor > 1.0f) || !isfinite(amp->growth_factor) || !(amp->backoff_factor > 0.0f) ||
+        !(amp->backoff_factor < 1.0f) || amp->growth_interval < 1 || !isfinite(amp->max_norm))
+      return fail(FP8ADAM_EINVAL, "growth_factor must exceed 1, backoff_factor lie in (0, 1), "
+                                  "growth_interval be >= 1 and max_norm be finite");
+    AdamwConsts C{};
+    group_consts(groups, n_groups, 0, C);
+    GroupRates R{};
+    for (int q = 0; q < n_groups; q++) {
+      R.lr[q] = groups[q].lr;
+      R.beta1[q] = groups[q].beta1;
+      R.beta2[q] = groups[q].beta2;
+    }
+    launch_sumsq(plan, stream);
+    HIP_TRY(hipGetLastError());
+    hipLaunchKernelGGL(k_list_ctl, dim3(1), dim3(kThreads), 0, stream, plan->d_partial, plan->norm_groups(), state,
+                       plan->d_ctl, *amp, R, n_groups);
+    HIP_TRY(hipGetLastError());
+    return run_adamw(plan, C, plan->d_ctl, stream);
+  });
+}
+
+int fp8adam_clip_grads(fp8adam_plan* plan, float max_norm, float* result, hipStream_t stream) {
+  return guarded("fp8adam_clip_grads", [&]() -> int {
+    if (int r = check_call(plan, kPlanClip, "fp8adam_clip_plan", stream)) return r;
+    if (!isfinite(max_norm)) return fail(FP8ADAM_EINVAL, "max_norm must be finite");
+    if (!result) return fail(FP8ADAM_EINVAL, "result is null");
+    if ((uintptr_t)result & 3u) return fail(FP8ADAM_EALIGN, "result is not 4-byte aligned");
+    launch_sumsq(plan, stream);
+    HIP_TRY(hipGetLastError());
+    hipLaunchKernelGGL(k_list_clip, dim3((unsigned)std::max(1, plan->norm_groups())), dim3(kThreads), 0, stream,
+                       plan->d_grad, plan->d_grad_tid, plan->grad_chunks, plan->grad_chunk_log2, plan->d_partial,
+                       plan->norm_groups(), max_norm, result);
+    HIP_TRY(hipGetLastError());
+    return 0;
+  });
+}
+
+int fp8adam_quantize(fp8adam_plan* plan, hipStream_t stream) {
+  return guarded("fp8adam_quantize", [&] { return convert(plan, false, stream); });
+}
+
+int fp8adam_dequantize(fp8adam_plan* plan, hipStream_t stream) {
+  return guarded("fp8adam_dequantize", [&] { return convert(plan, true, stream); });
+}
+
+}  // extern "C"

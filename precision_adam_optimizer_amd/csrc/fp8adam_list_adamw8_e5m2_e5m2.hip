@@ -1,0 +1,10 @@
+// fp8adam_list_adamw8_e5m2_e5m2.hip -- instantiates the list AdamW kernels with 8-bit moments, m in E5M2
+// and v in E5M2 (one translation unit per format pair, so the library builds in parallel).
+#include "fp8adam_list.h"
+
+namespace fp8adam_list {
+
+template void launch_adamw<true, 1, 1>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&, int64_t,
+                                         const AdamwCtl*, hipStream_t);
+
+}  // namespace fp8adam_list
