@@ -59,6 +59,51 @@ __device__ __forceinline__ void st_elem(void* base, int64_t i, float x) {
   else st_global<uint16_t>(static_cast<uint16_t*>(base) + i, __builtin_bit_cast(uint16_t, to_f16(x)));
 }
 
+// Four consecutive elements through a buffer resource, at element offset o of its
+// base (dword-aligned: 16 bytes of fp32 or 8 of a 16-bit type per lane).
+template <int DT> struct Raw4 { vu2 x; };
+template <> struct Raw4<FP8ADAM_F32> { vu4 x; };
+
+template <int DT>
+__device__ __forceinline__ Rsrc typed_rsrc(const void* base, int64_t first, int64_t n) {
+  constexpr int64_t B = DT == FP8ADAM_F32 ? 4 : 2;
+  return rsrc(static_cast<const char*>(base) + B * first, B * n);
+}
+
+template <int DT, int POL = kLdPol>
+__device__ __forceinline__ Raw4<DT> load4(Rsrc r, uint32_t o) {
+  if constexpr (DT == FP8ADAM_F32) return Raw4<DT>{__builtin_amdgcn_raw_buffer_load_b128(r, 4 * o, 0, POL)};
+  else return Raw4<DT>{__builtin_amdgcn_raw_buffer_load_b64(r, 2 * o, 0, POL)};
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack4(const Raw4<DT>& w, float (&x)[4]) {
+  if constexpr (DT == FP8ADAM_F32) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) x[j] = __uint_as_float(w.x[j]);
+  } else if constexpr (DT == FP8ADAM_BF16) {
+    x[0] = bf16_lo(w.x.x); x[1] = bf16_hi(w.x.x); x[2] = bf16_lo(w.x.y); x[3] = bf16_hi(w.x.y);
+  } else {
+    const uint32_t lo = w.x.x, hi = w.x.y;  // (a bit cast of a vector's component takes the vector's first)
+    const f16x2 a = __builtin_bit_cast(f16x2, lo), b = __builtin_bit_cast(f16x2, hi);
+    x[0] = (float)a[0]; x[1] = (float)a[1]; x[2] = (float)b[0]; x[3] = (float)b[1];
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (DT == FP8ADAM_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(vf2{a, b}, bf16x2));
+  else return __builtin_bit_cast(uint32_t, f16x2{to_f16(a), to_f16(b)});
+}
+
+template <int DT, int POL = kStPol>
+__device__ __forceinline__ void store4(Rsrc r, uint32_t o, const float (&x)[4]) {
+  if constexpr (DT == FP8ADAM_F32)
+    __builtin_amdgcn_raw_buffer_store_b128(
+        vu4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])}, r, 4 * o, 0, POL);
+  else __builtin_amdgcn_raw_buffer_store_b64(vu2{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])}, r, 2 * o, 0, POL);
+}
+
 // The codes of four values, to nearest even, saturating, where a NaN stays one
 // (the clamp of encode4 alone would make it -FMAX).  `odd`: the values' block or
 // tensor holds a NaN or Inf, which its amax tells; without one the test is not
@@ -89,7 +134,8 @@ struct AdamwDesc {
   int64_t numel;
   int64_t part0;   // the tensor's first part in its kind's table
   int32_t group;
-  int32_t pad;
+  int16_t head;    // elements in front of the first part (0 or 1), which the first part's work-group does alone
+  int16_t vec;     // every stream starts on a dword at element `head`
 };
 
 // One parameter group's constants, computed on the host from its hyperparameters.
@@ -130,16 +176,52 @@ __device__ __forceinline__ float adamw_element(const GroupConsts& c, float g, fl
   return p - __builtin_fmaf(c.lr_wd, p, upd);
 }
 
-// Elements of an AdamW part: 256 lanes of 4.
-constexpr int kAdamwPartLog2 = 10;
+// log2 of a part's elements: 256 lanes of 4, twice where an element moves few bytes.
+#ifndef ADAMW_WIDE
+#define ADAMW_WIDE 11
+#endif
+#ifndef ADAMW_32
+#define ADAMW_32 10
+#endif
+#ifndef ADAMW_8
+#define ADAMW_8 10
+#endif
+constexpr int adamw_part_log2(int pd, bool s8) { return s8 ? pd != FP8ADAM_F32 ? ADAMW_WIDE : ADAMW_8 : ADAMW_32; }
+
+// The moments of a run of 128 elements that 32 lanes own, four each: new scales
+// and codes.
+template <int MF, int VF>
+__device__ __forceinline__ void moments_to_codes(const float (&m1)[4], const float (&v1)[4], float& sm, float& sv,
+                                                 uint32_t& wm, uint32_t& wv) {
+  float ism, isv;
+  uint32_t am = 0, av = 0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    am = max(am, abs_bits(m1[j]));
+    av = max(av, abs_bits(v1[j]));
+  }
+  am = group32_max(am);
+  av = group32_max(av);
+  choose_scale<MF, 0>(am, sm, ism);
+  choose_scale<VF, 0>(av, sv, isv);
+  const float qm[4] = {m1[0] * ism, m1[1] * ism, m1[2] * ism, m1[3] * ism};
+  const float qv[4] = {v1[0] * isv, v1[1] * isv, v1[2] * isv, v1[3] * isv};
+  wm = encode4_nan<MF>(qm, nonfinite_amax(am));
+  wv = encode4_nan<VF>(qv, nonfinite_amax(av));
+}
 
 // One work-group per part.  32 lanes own one run of 128 elements (a block of
-// 8-bit moments): lane h holds its elements h, h + 32, h + 64 and h + 96, so
-// every access of a wave is contiguous at any alignment.
+// 8-bit moments).  A whole part of a tensor whose streams start on dwords goes in
+// groups of four consecutive elements per lane, through buffer resources; another
+// one element by element, where lane h of the 32 holds elements h, h + 32, h + 64
+// and h + 96 of its run, so that accesses are contiguous at any alignment.
 template <int PD, int CD, int GD, bool S8, int MF, int VF>
 __global__ __launch_bounds__(kThreads) void k_adamw(const AdamwDesc* __restrict__ descs,
                                                     const int32_t* __restrict__ part_tid, AdamwConsts C, int64_t nparts,
                                                     const AdamwCtl* __restrict__ ctl) {
+  constexpr int PL = adamw_part_log2(PD, S8);
+  constexpr int64_t kLen = (int64_t)1 << PL;
+  constexpr int kU = (int)(kLen / kSubTile);
   const int64_t w = work_index<kXcdStreams>(nparts);
   if (w < 0) return;
   const AdamwDesc d = descs[part_tid[w]];
@@ -151,69 +233,133 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamwDesc* __restrict_
     c.step_size = ctl->step_size[d.group];
     c.inv_bc2 = ctl->inv_bc2[d.group];
   }
-  const int64_t block = ((w - d.part0) << (kAdamwPartLog2 - 7)) + (threadIdx.x >> 5);
-  const int64_t i0 = block * kBlock + (threadIdx.x & 31);
-  const bool any = block * kBlock < d.numel;  // uniform for the 32 lanes
-  float sm = 1.0f, sv = 1.0f;
-  if constexpr (S8) {
-    if (any) {
-      sm = ld_global<float>(d.sm + block);
-      sv = ld_global<float>(d.sv + block);
-    }
-  }
-  float p[4], m1[4], v1[4];
+  const int64_t lo = d.head + ((w - d.part0) << PL);
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;  // of 8 runs per tile of 1024
+  if (d.vec && lo + kLen <= d.numel) {
+    const Rsrc bp = typed_rsrc<PD>(d.p, lo, kLen), bg = typed_rsrc<GD>(d.g, lo, kLen);
+    const Rsrc bm = S8 ? rsrc(static_cast<uint8_t*>(d.m) + lo, kLen) : typed_rsrc<FP8ADAM_F32>(d.m, lo, kLen);
+    const Rsrc bv = S8 ? rsrc(static_cast<uint8_t*>(d.v) + lo, kLen) : typed_rsrc<FP8ADAM_F32>(d.v, lo, kLen);
+    Raw4<PD> rp[kU];
+    Raw4<GD> rg[kU];
+    Raw4<FP8ADAM_F32> rm[kU], rv[kU];
+    uint32_t cm[kU], cv[kU];
+    float sm[kU], sv[kU];
+    const int64_t block0 = (lo >> 7) + run;
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const int64_t i = i0 + 32 * j;
-    p[j] = m1[j] = v1[j] = 0.0f;
-    if (i < d.numel) {
-      const float g = ld_elem<GD>(d.g, i) * gfac;
-      float m, v;
+    for (int u = 0; u < kU; u++) {
+      const uint32_t o = 4 * threadIdx.x + u * kSubTile;
+      rg[u] = load4<GD>(bg, o);
       if constexpr (S8) {
-        m = decode1<MF>(ld_global<uint8_t>(static_cast<const uint8_t*>(d.m) + i)) * sm;
-        v = decode1<VF>(ld_global<uint8_t>(static_cast<const uint8_t*>(d.v) + i)) * sv;
+        cm[u] = __builtin_amdgcn_raw_buffer_load_b32(bm, o, 0, kLdPol);
+        cv[u] = __builtin_amdgcn_raw_buffer_load_b32(bv, o, 0, kLdPol);
+        sm[u] = ld_global<float>(d.sm + block0 + 8 * u);
+        sv[u] = ld_global<float>(d.sv + block0 + 8 * u);
       } else {
-        m = ld_global<float>(static_cast<const float*>(d.m) + i);
-        v = ld_global<float>(static_cast<const float*>(d.v) + i);
+        rm[u] = load4<FP8ADAM_F32>(bm, o);
+        rv[u] = load4<FP8ADAM_F32>(bv, o);
       }
-      p[j] = adamw_element(c, g, ld_elem<PD>(d.p, i), m, v, m1[j], v1[j]);
+      rp[u] = load4<PD>(bp, o);
     }
-  }
-  uint32_t wm = 0, wv = 0;
-  if constexpr (S8) {
-    float ism, isv;
-    uint32_t am = 0, av = 0;
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      am = max(am, abs_bits(m1[j]));
-      av = max(av, abs_bits(v1[j]));
-    }
-    am = group32_max(am);
-    av = group32_max(av);
-    choose_scale<MF, 0>(am, sm, ism);
-    choose_scale<VF, 0>(av, sv, isv);
-    if (any && (threadIdx.x & 31) == 0) {
-      st_global<float>(d.sm + block, sm);
-      st_global<float>(d.sv + block, sv);
-    }
-    const float qm[4] = {m1[0] * ism, m1[1] * ism, m1[2] * ism, m1[3] * ism};
-    const float qv[4] = {v1[0] * isv, v1[1] * isv, v1[2] * isv, v1[3] * isv};
-    wm = encode4_nan<MF>(qm, nonfinite_amax(am));
-    wv = encode4_nan<VF>(qv, nonfinite_amax(av));
-  }
-#pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const int64_t i = i0 + 32 * j;
-    if (i < d.numel) {
-      st_elem<PD>(d.p, i, p[j]);
-      if constexpr (CD != 0) st_elem<CD>(d.copy, i, p[j]);
+    for (int u = 0; u < kU; u++) {
+      const uint32_t o = 4 * threadIdx.x + u * kSubTile;
+      float p[4], g[4], m[4], v[4], m1[4], v1[4];
+      unpack4<GD>(rg[u], g);
       if constexpr (S8) {
-        st_global<uint8_t>(static_cast<uint8_t*>(d.m) + i, (uint8_t)(wm >> (8 * j)));
-        st_global<uint8_t>(static_cast<uint8_t*>(d.v) + i, (uint8_t)(wv >> (8 * j)));
+        decode4<MF>(cm[u], m);
+        decode4<VF>(cv[u], v);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          m[j] *= sm[u];
+          v[j] *= sv[u];
+        }
       } else {
-        st_global<float>(static_cast<float*>(d.m) + i, m1[j]);
-        st_global<float>(static_cast<float*>(d.v) + i, v1[j]);
+        unpack4<FP8ADAM_F32>(rm[u], m);
+        unpack4<FP8ADAM_F32>(rv[u], v);
       }
+      unpack4<PD>(rp[u], p);
+#pragma unroll
+      for (int j = 0; j < 4; j++) p[j] = adamw_element(c, g[j] * gfac, p[j], m[j], v[j], m1[j], v1[j]);
+      store4<PD>(bp, o, p);
+      if constexpr (CD != 0) store4<CD>(typed_rsrc<CD>(d.copy, lo, kLen), o, p);
+      if constexpr (S8) {
+        uint32_t wm, wv;
+        float ns, nv;
+        moments_to_codes<MF, VF>(m1, v1, ns, nv, wm, wv);
+        __builtin_amdgcn_raw_buffer_store_b32(wm, bm, o, 0, kStPol);
+        __builtin_amdgcn_raw_buffer_store_b32(wv, bv, o, 0, kStPol);
+        if (lane == 0) {
+          st_global<float>(d.sm + block0 + 8 * u, ns);
+          st_global<float>(d.sv + block0 + 8 * u, nv);
+        }
+      } else {
+        store4<FP8ADAM_F32>(bm, o, m1);
+        store4<FP8ADAM_F32>(bv, o, v1);
+      }
+    }
+  } else {
+    for (int u = 0; u < kU; u++) {
+      const int64_t first = lo + u * kSubTile + run * kBlock, block = first >> 7;
+      const bool any = first < d.numel;  // uniform for the 32 lanes
+      float sm = 1.0f, sv = 1.0f;
+      if constexpr (S8) {
+        if (any) {
+          sm = ld_global<float>(d.sm + block);
+          sv = ld_global<float>(d.sv + block);
+        }
+      }
+      float p[4], m1[4], v1[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int64_t i = first + lane + 32 * j;
+        p[j] = m1[j] = v1[j] = 0.0f;
+        if (i < d.numel) {
+          const float g = ld_elem<GD>(d.g, i) * gfac;
+          float m, v;
+          if constexpr (S8) {
+            m = decode1<MF>(ld_global<uint8_t>(static_cast<const uint8_t*>(d.m) + i)) * sm;
+            v = decode1<VF>(ld_global<uint8_t>(static_cast<const uint8_t*>(d.v) + i)) * sv;
+          } else {
+            m = ld_global<float>(static_cast<const float*>(d.m) + i);
+            v = ld_global<float>(static_cast<const float*>(d.v) + i);
+          }
+          p[j] = adamw_element(c, g, ld_elem<PD>(d.p, i), m, v, m1[j], v1[j]);
+        }
+      }
+      uint32_t wm = 0, wv = 0;
+      if constexpr (S8) {
+        moments_to_codes<MF, VF>(m1, v1, sm, sv, wm, wv);
+        if (any && lane == 0) {
+          st_global<float>(d.sm + block, sm);
+          st_global<float>(d.sv + block, sv);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int64_t i = first + lane + 32 * j;
+        if (i < d.numel) {
+          st_elem<PD>(d.p, i, p[j]);
+          if constexpr (CD != 0) st_elem<CD>(d.copy, i, p[j]);
+          if constexpr (S8) {
+            st_global<uint8_t>(static_cast<uint8_t*>(d.m) + i, (uint8_t)(wm >> (8 * j)));
+            st_global<uint8_t>(static_cast<uint8_t*>(d.v) + i, (uint8_t)(wv >> (8 * j)));
+          } else {
+            st_global<float>(static_cast<float*>(d.m) + i, m1[j]);
+            st_global<float>(static_cast<float*>(d.v) + i, v1[j]);
+          }
+        }
+      }
+    }
+  }
+  if constexpr (!S8) {
+    if (d.head && w == d.part0 && threadIdx.x == 0) {
+      float m1, v1;
+      const float p = adamw_element(c, ld_elem<GD>(d.g, 0) * gfac, ld_elem<PD>(d.p, 0),
+                                    ld_global<float>(d.m), ld_global<float>(d.v), m1, v1);
+      st_elem<PD>(d.p, 0, p);
+      if constexpr (CD != 0) st_elem<CD>(d.copy, 0, p);
+      st_global<float>(d.m, m1);
+      st_global<float>(d.v, v1);
     }
   }
 }

@@ -45,12 +45,53 @@ struct GradDesc {
   int32_t sdt, ddt;
 };
 
-constexpr int kListNormGroups = 2048;  // 8 work-groups per CU
+// Two work-groups per CU with 8 16-byte loads per lane keep the norm pass at the
+// read-only rate (7.0 TB/s), and the clipping pass, whose every work-group sums
+// the partials, reads few of them: clipping 842M fp32 gradients to bf16 takes 1264
+// us with 512, 1284 with 2048.
+constexpr int kListNormGroups = 512;
 
+__device__ __forceinline__ void sumsq_word(uint32_t x, double& acc, std::integral_constant<int, FP8ADAM_F32>) {
+  const double a = __uint_as_float(x);
+  acc = __builtin_fma(a, a, acc);
+}
+__device__ __forceinline__ void sumsq_word(uint32_t x, double& acc, std::integral_constant<int, FP8ADAM_BF16>) {
+  const double a = bf16_lo(x), b = bf16_hi(x);
+  acc = __builtin_fma(a, a, acc);
+  acc = __builtin_fma(b, b, acc);
+}
+__device__ __forceinline__ void sumsq_word(uint32_t x, double& acc, std::integral_constant<int, FP8ADAM_F16>) {
+  const f16x2 h = __builtin_bit_cast(f16x2, x);
+  const double a = (float)h[0], b = (float)h[1];
+  acc = __builtin_fma(a, a, acc);
+  acc = __builtin_fma(b, b, acc);
+}
+
+// The squares of elements [lo, hi): single ones up to a 16-byte boundary, then
+// 16-byte loads, kSumUnroll in flight per lane (the buffer resource ends with the
+// last whole vector: a load behind it gives zeros, which add nothing), then the
+// rest.
+constexpr int kSumUnroll = 8;
 template <int DT>
 __device__ __forceinline__ void sumsq_range(const void* src, int64_t lo, int64_t hi, double& acc) {
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-    const double x = ld_elem<DT>(src, i);
+  constexpr int kBytes = DT == FP8ADAM_F32 ? 4 : 2, kVec = 16 / kBytes;
+  const char* base = static_cast<const char*>(src) + kBytes * lo;
+  const int n = (int)(hi - lo);
+  const int head = min(n, (int)((16u - ((uintptr_t)base & 15u)) & 15u) / kBytes);
+  const int nvec = (n - head) / kVec, tail = head + nvec * kVec;
+  const Rsrc r = rsrc(base + kBytes * head, 16 * (int64_t)nvec);
+  for (int v = threadIdx.x; v < nvec; v += kThreads * kSumUnroll) {
+    vu4 x[kSumUnroll];
+#pragma unroll
+    for (int u = 0; u < kSumUnroll; u++) x[u] = __builtin_amdgcn_raw_buffer_load_b128(r, 16 * (v + u * kThreads), 0, kLdPol);
+#pragma unroll
+    for (int u = 0; u < kSumUnroll; u++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) sumsq_word(x[u][j], acc, std::integral_constant<int, DT>{});
+  }
+  const int single = (int)threadIdx.x < head ? (int)threadIdx.x : tail + (int)threadIdx.x - head;
+  if (single < n) {  // at most 7 in front and 7 behind
+    const double x = ld_elem<DT>(base, single);
     acc = __builtin_fma(x, x, acc);
   }
 }
@@ -84,49 +125,13 @@ __global__ __launch_bounds__(kThreads) void k_list_sumsq(const GradDesc* __restr
   if (threadIdx.x == 0) partial[blockIdx.x] = acc;
 }
 
-// The whole sum from the partials: the same order in every work-group that asks.
+// The whole sum from the partials, in every thread: the same order in every
+// work-group that asks.
 __device__ __forceinline__ double total_of(const double* __restrict__ partial, int n) {
   double acc = 0.0;
+#pragma unroll 4
   for (int k = threadIdx.x; k < n; k += kThreads) acc += partial[k];
   return block_sum(acc);
-}
-
-template <int SD, int DD>
-__device__ __forceinline__ void scale_range(const GradDesc& d, int64_t lo, int64_t hi, float coef) {
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) st_elem<DD>(d.dst, i, ld_elem<SD>(d.src, i) * coef);
-}
-
-template <int SD>
-__device__ __forceinline__ void scale_range_to(const GradDesc& d, int64_t lo, int64_t hi, float coef) {
-  if (d.ddt == FP8ADAM_F32) scale_range<SD, FP8ADAM_F32>(d, lo, hi, coef);
-  else if (d.ddt == FP8ADAM_BF16) scale_range<SD, FP8ADAM_BF16>(d, lo, hi, coef);
-  else scale_range<SD, FP8ADAM_F16>(d, lo, hi, coef);
-}
-
-__global__ __launch_bounds__(kThreads) void k_list_clip(const GradDesc* __restrict__ descs,
-                                                        const int32_t* __restrict__ chunk_tid, int64_t nchunks,
-                                                        int chunk_log2, const double* __restrict__ partial, int npartial,
-                                                        float max_norm, float* __restrict__ result) {
-  const double norm = __dsqrt_rn(total_of(partial, npartial));
-  double cc = 1.0;
-  if (max_norm > 0.0f && isfinite(norm)) {
-    cc = __ddiv_rn((double)max_norm, __dadd_rn(norm, 1e-6));
-    if (cc > 1.0) cc = 1.0;
-  }
-  const float coef = __double2float_rn(cc);
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    st_global<float>(result, __double2float_rn(norm));
-    st_global<float>(result + 1, coef);
-  }
-  for (int64_t w = blockIdx.x; w < nchunks; w += gridDim.x) {
-    const GradDesc d = descs[chunk_tid[w]];
-    if (d.dst == nullptr || (coef == 1.0f && d.dst == d.src)) continue;  // uniform: nothing to write, or nothing changes
-    const int64_t lo = (w - d.chunk0) << chunk_log2;
-    const int64_t hi = min(lo + ((int64_t)1 << chunk_log2), d.numel);
-    if (d.sdt == FP8ADAM_F32) scale_range_to<FP8ADAM_F32>(d, lo, hi, coef);
-    else if (d.sdt == FP8ADAM_BF16) scale_range_to<FP8ADAM_BF16>(d, lo, hi, coef);
-    else scale_range_to<FP8ADAM_F16>(d, lo, hi, coef);
-  }
 }
 
 // Loss scaling: the scaler's decision, and each group's bias corrections at the
@@ -154,6 +159,83 @@ __global__ __launch_bounds__(kThreads) void k_list_ctl(const double* __restrict_
     ctl->step_size[q] = (float)(R.lr[q] / (1.0 - pow(R.beta1[q], (double)t_now)));
     ctl->inv_bc2[q] = (float)(1.0 / (1.0 - pow(R.beta2[q], (double)t_now)));
   }
+}
+
+constexpr int kClipUnroll = 4;
+
+// dst = src * coef over [lo, hi).  Groups of four elements per lane wherever every
+// group starts on a dword in both, after one single element where the 16-bit
+// pointers are both off by one; element by element otherwise (two 16-bit types of
+// which one is off by one).
+template <int SD, int DD>
+__device__ __forceinline__ void scale_range(const GradDesc& d, int64_t lo, int64_t hi, float coef) {
+  constexpr int SB = SD == FP8ADAM_F32 ? 4 : 2, DB = DD == FP8ADAM_F32 ? 4 : 2;
+  const char* src = static_cast<const char*>(d.src) + SB * lo;
+  char* dst = static_cast<char*>(d.dst) + DB * lo;
+  const int n = (int)(hi - lo);
+  const int soff = SB == 2 ? (int)((uintptr_t)src >> 1 & 1u) : -1, doff = DB == 2 ? (int)((uintptr_t)dst >> 1 & 1u) : -1;
+  const int head = max(max(soff, doff), 0);
+  if (soff >= 0 && doff >= 0 && soff != doff) {  // uniform
+    for (int i = threadIdx.x; i < n; i += kThreads) st_elem<DD>(dst, i, ld_elem<SD>(src, i) * coef);
+    return;
+  }
+  const int nvec = max(n - head, 0) >> 2, tail = head + 4 * nvec;
+  const Rsrc rs = typed_rsrc<SD>(src, head, 4 * nvec), rd = typed_rsrc<DD>(dst, head, 4 * nvec);
+  for (int v = threadIdx.x; v < nvec; v += kThreads * kClipUnroll) {
+    Raw4<SD> w[kClipUnroll];
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; u++) w[u] = load4<SD>(rs, 4 * (v + u * kThreads));
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; u++) {
+      float x[4];
+      unpack4<SD>(w[u], x);
+#pragma unroll
+      for (int j = 0; j < 4; j++) x[j] *= coef;
+      store4<DD>(rd, 4 * (v + u * kThreads), x);  // one behind the last vector is dropped
+    }
+  }
+  const int single = (int)threadIdx.x < head ? (int)threadIdx.x : tail + (int)threadIdx.x - head;
+  if (single < n) st_elem<DD>(dst, single, ld_elem<SD>(src, single) * coef);
+}
+
+template <int SD>
+__device__ __forceinline__ void scale_range_to(const GradDesc& d, int64_t lo, int64_t hi, float coef) {
+  if (d.ddt == FP8ADAM_F32) scale_range<SD, FP8ADAM_F32>(d, lo, hi, coef);
+  else if (d.ddt == FP8ADAM_BF16) scale_range<SD, FP8ADAM_BF16>(d, lo, hi, coef);
+  else scale_range<SD, FP8ADAM_F16>(d, lo, hi, coef);
+}
+
+// One work-group per 2^kClipPartLog2 elements, from the list's end to its start:
+// what the norm pass read last may still be in the last-level cache.
+constexpr int kClipPartLog2 = 12;
+constexpr int kGradChunkMinLog2 = 12, kGradChunkMaxLog2 = 15;
+static_assert(kClipPartLog2 <= kGradChunkMinLog2, "a chunk holds whole parts");
+
+__global__ __launch_bounds__(kThreads) void k_list_clip(const GradDesc* __restrict__ descs,
+                                                        const int32_t* __restrict__ chunk_tid, int64_t nparts,
+                                                        int chunk_log2, const double* __restrict__ partial, int npartial,
+                                                        float max_norm, float* __restrict__ result) {
+  const double norm = __dsqrt_rn(total_of(partial, npartial));
+  double cc = 1.0;
+  if (max_norm > 0.0f && isfinite(norm)) {
+    cc = __ddiv_rn((double)max_norm, __dadd_rn(norm, 1e-6));
+    if (cc > 1.0) cc = 1.0;
+  }
+  const float coef = __double2float_rn(cc);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    st_global<float>(result, __double2float_rn(norm));
+    st_global<float>(result + 1, coef);
+  }
+  if (nparts == 0) return;  // nothing is written
+  const int64_t w = nparts - 1 - (int64_t)blockIdx.x;
+  const GradDesc d = descs[chunk_tid[w >> (chunk_log2 - kClipPartLog2)]];
+  if (d.dst == nullptr || (coef == 1.0f && d.dst == d.src)) return;  // uniform: nothing to write, or nothing changes
+  const int64_t lo = (w - (d.chunk0 << (chunk_log2 - kClipPartLog2))) << kClipPartLog2;
+  const int64_t hi = min(lo + ((int64_t)1 << kClipPartLog2), d.numel);
+  if (lo >= hi) return;  // behind the tensor's end, in its last chunk
+  if (d.sdt == FP8ADAM_F32) scale_range_to<FP8ADAM_F32>(d, lo, hi, coef);
+  else if (d.sdt == FP8ADAM_BF16) scale_range_to<FP8ADAM_BF16>(d, lo, hi, coef);
+  else scale_range_to<FP8ADAM_F16>(d, lo, hi, coef);
 }
 
 // -------------------------------------------------------- conversion to 8 bits
@@ -350,6 +432,7 @@ struct fp8adam_plan {
   const int32_t* d_grad_tid = nullptr;
   int64_t grad_chunks = 0;
   int grad_chunk_log2 = 0;
+  int64_t clip_parts = 0;                 // clipping: work-groups of the second pass (0: nothing is written)
   double* d_partial = nullptr;
   AdamwCtl* d_ctl = nullptr;
   uint32_t* d_amax = nullptr;             // conversion with per-tensor scales: one per chunk
@@ -413,8 +496,8 @@ int check_call(const fp8adam_plan* p, PlanKind kind, const char* what, hipStream
 // Chunks of the gradient list: the largest power of two of 4096 .. 32768
 // elements that still gives the norm pass a work-group for each of its places.
 void chunk_grads(std::vector<GradDesc>& g, int64_t total, int& chunk_log2, std::vector<int32_t>& tid) {
-  chunk_log2 = 15;
-  while (chunk_log2 > 12 && (total >> chunk_log2) < kListNormGroups) chunk_log2--;
+  chunk_log2 = kGradChunkMaxLog2;
+  while (chunk_log2 > kGradChunkMinLog2 && (total >> chunk_log2) < kListNormGroups) chunk_log2--;
   for (size_t t = 0; t < g.size(); t++) {
     g[t].chunk0 = (int64_t)tid.size();
     const int64_t nc = (g[t].numel + ((int64_t)1 << chunk_log2) - 1) >> chunk_log2;
@@ -573,9 +656,22 @@ int adamw_plan(fp8adam_plan** out, const fp8adam_adamw_tensor* T, int32_t n, con
   for (int32_t t = 0; t < n; t++) {
     const fp8adam_adamw_tensor& x = T[t];
     grads[t] = GradDesc{x.grad, nullptr, x.numel, 0, x.grad_dtype, 0};
-    desc[t] = AdamwDesc{x.param, x.grad, x.copy, x.m, x.v, x.m_scale, x.v_scale, x.numel, 0, x.group, 0};
+    const bool s8 = x.moments == FP8ADAM_MOMENTS_8;
+    desc[t] = AdamwDesc{x.param, x.grad, x.copy, x.m, x.v, x.m_scale, x.v_scale, x.numel, 0, x.group, 0, 0};
     if (x.numel == 0) continue;
-    const AdamwKind kind{x.param_dtype, x.copy ? x.copy_dtype : 0, x.grad_dtype, x.moments == FP8ADAM_MOMENTS_8};
+    const AdamwKind kind{x.param_dtype, x.copy ? x.copy_dtype : 0, x.grad_dtype, s8};
+    // Streams that start on dwords: fp32 ones always do; 16-bit ones with 32-bit moments either at
+    // element 0 or, if all are off by one, at element 1; blocks of codes start at element 0.
+    auto odd = [](const void* q, int dt) { return dt == FP8ADAM_F32 ? -1 : (int)((uintptr_t)q >> 1 & 1); };
+    int off = -1;
+    bool vec = !s8 || (((uintptr_t)x.m | (uintptr_t)x.v) & 3u) == 0;
+    for (int o : {odd(x.param, x.param_dtype), odd(x.grad, x.grad_dtype), x.copy ? odd(x.copy, x.copy_dtype) : -1}) {
+      vec = vec && (o < 0 || off < 0 || o == off);
+      off = std::max(off, o);
+    }
+    vec = vec && !(s8 && off == 1);
+    desc[t].vec = vec ? 1 : 0;
+    desc[t].head = vec && off == 1 ? 1 : 0;
     auto it = std::find_if(p->spans.begin(), p->spans.end(), [&](const Span& k) { return k.kind == kind; });
     if (it == p->spans.end()) {
       p->spans.emplace_back();
@@ -583,7 +679,8 @@ int adamw_plan(fp8adam_plan** out, const fp8adam_adamw_tensor* T, int32_t n, con
       it->kind = kind;
     }
     desc[t].part0 = (int64_t)it->tid.size();
-    const int64_t parts = (x.numel + ((int64_t)1 << kAdamwPartLog2) - 1) >> kAdamwPartLog2;
+    const int pl = adamw_part_log2(x.param_dtype, s8);
+    const int64_t parts = std::max<int64_t>(1, (x.numel - desc[t].head + ((int64_t)1 << pl) - 1) >> pl);
     if (int r = check_parts(desc[t].part0 + parts)) return r;
     it->tid.insert(it->tid.end(), (size_t)parts, t);
   }
@@ -641,6 +738,9 @@ int clip_plan(fp8adam_plan** out, const fp8adam_clip_tensor* T, int32_t n, hipSt
   std::vector<int32_t> gtid;
   chunk_grads(grads, total, p->grad_chunk_log2, gtid);
   p->grad_chunks = (int64_t)gtid.size();
+  if (std::any_of(grads.begin(), grads.end(), [](const GradDesc& g) { return g.numel > 0 && g.dst; }))
+    p->clip_parts = p->grad_chunks << (p->grad_chunk_log2 - kClipPartLog2);
+  if (int r = check_parts(p->clip_parts)) return r;
   if (int r = plan_device(p, stream)) return r;
   Image im;
   const size_t at_grad = im.put(grads.data(), sizeof(GradDesc) * grads.size());
@@ -828,8 +928,8 @@ int fp8adam_clip_grads(fp8adam_plan* plan, float max_norm, float* result, hipStr
     if ((uintptr_t)result & 3u) return fail(FP8ADAM_EALIGN, "result is not 4-byte aligned");
     launch_sumsq(plan, stream);
     HIP_TRY(hipGetLastError());
-    hipLaunchKernelGGL(k_list_clip, dim3((unsigned)std::max(1, plan->norm_groups())), dim3(kThreads), 0, stream,
-                       plan->d_grad, plan->d_grad_tid, plan->grad_chunks, plan->grad_chunk_log2, plan->d_partial,
+    hipLaunchKernelGGL(k_list_clip, dim3((unsigned)std::max<int64_t>(1, plan->clip_parts)), dim3(kThreads), 0, stream,
+                       plan->d_grad, plan->d_grad_tid, plan->clip_parts, plan->grad_chunk_log2, plan->d_partial,
                        plan->norm_groups(), max_norm, result);
     HIP_TRY(hipGetLastError());
     return 0;
