@@ -246,14 +246,22 @@ struct QuantDesc {
   float* scale;
   int64_t numel;
   int64_t part0;
-  int64_t chunk0;    // per-tensor scales: its first amax chunk, their number and length
-  int64_t nchunks;
+  int64_t chunk0;    // per-tensor scales: its first amax chunk, the chunks' length
   int64_t chunk_len;
+  int64_t slot0;     // the first slot of their maxima, a multiple of 4; unused slots up to the next tensor hold 0
+  int32_t slots;     // their number, a multiple of 4
+  int32_t head;      // per-tensor scales: elements in front of the first part (0 .. 3)
+  int32_t vec;       // values and codes both start on a dword at element `head`
 };
 
-constexpr int kQuantPartLog2 = 10;        // elements of a block-scaled or dequantizing work-group
-constexpr int kQuantTensorPartLog2 = 13;  // of one that quantizes with a tensor's scale
-constexpr int64_t kAmaxMaxChunks = 512;   // amax chunks per tensor at most (each quantizing work-group reads them all)
+// log2 of the elements of a one-shot work-group.  Blocks, both ways: 2048 (109.5M
+// fp32 to E4M3 blocks 83 us, back 93 us; 1024: 93 and 99, 4096: 85 and 98, 8192: 91
+// and 103).  With a tensor's scale: 4096 (202M bf16 in 150 us; 2048: 161, 8192: 153),
+// since each wave reads the tensor's maxima first.
+constexpr int kQuantPartLog2 = 11;
+constexpr int kQuantTensorPartLog2 = 12;
+// Amax chunks per tensor at most: each quantizing wave reads them all, with one 16-byte load per lane.
+constexpr int64_t kAmaxMaxChunks = 256;
 constexpr int64_t kAmaxMinChunk = 8192;
 
 template <int FMT>
@@ -262,83 +270,184 @@ __device__ __forceinline__ void choose_scale_mode(uint32_t amax, int smode, floa
   else choose_scale<FMT, 1>(amax, s, inv);
 }
 
-// One work-group per part, 32 lanes per block of 128 (lane h: its elements h,
-// h + 32, h + 64, h + 96).
+// The new scale and the codes of a run of 128 values that 32 lanes hold, four each.
+template <int FMT>
+__device__ __forceinline__ uint32_t block_to_codes(float (&x)[4], int smode, float& s) {
+  uint32_t am = 0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) am = max(am, abs_bits(x[j]));
+  am = group32_max(am);
+  float inv;
+  choose_scale_mode<FMT>(am, smode, s, inv);
+#pragma unroll
+  for (int j = 0; j < 4; j++) x[j] *= inv;
+  return encode4_nan<FMT>(x, nonfinite_amax(am));
+}
+
+// One work-group per part, 32 lanes per block of 128, four consecutive elements
+// per lane; in a part that is not whole or not dword-aligned lane h takes the
+// block's elements h, h + 32, h + 64, h + 96.
 template <int DT, int FMT>
 __global__ __launch_bounds__(kThreads) void k_quant_block(const QuantDesc* __restrict__ descs,
                                                           const int32_t* __restrict__ part_tid, int64_t nparts,
                                                           int smode) {
-  const int64_t w = work_index<kXcdStreams>(nparts);
+  constexpr int64_t kLen = (int64_t)1 << kQuantPartLog2;
+  constexpr int kU = (int)(kLen / kSubTile);
+  const int64_t w = run_index(nparts);
   if (w < 0) return;
   const QuantDesc d = descs[part_tid[w]];
-  const int64_t block = ((w - d.part0) << (kQuantPartLog2 - 7)) + (threadIdx.x >> 5);
-  const int64_t i0 = block * kBlock + (threadIdx.x & 31);
-  float x[4];
-  uint32_t am = 0;
+  const int64_t lo = (w - d.part0) << kQuantPartLog2;
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+  if (d.vec && lo + kLen <= d.numel) {
+    const Rsrc bx = typed_rsrc<DT>(d.x, lo, kLen), bc = rsrc(d.codes + lo, kLen);
+    Raw4<DT> r[kU];
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    x[j] = i0 + 32 * j < d.numel ? ld_elem<DT>(d.x, i0 + 32 * j) : 0.0f;
-    am = max(am, abs_bits(x[j]));
+    for (int u = 0; u < kU; u++) r[u] = load4<DT>(bx, 4 * threadIdx.x + u * kSubTile);
+#pragma unroll
+    for (int u = 0; u < kU; u++) {
+      float x[4], s;
+      unpack4<DT>(r[u], x);
+      const uint32_t codes = block_to_codes<FMT>(x, smode, s);
+      __builtin_amdgcn_raw_buffer_store_b32(codes, bc, 4 * threadIdx.x + u * kSubTile, 0, kStPol);
+      if (lane == 0) st_global<float>(d.scale + (lo >> 7) + 8 * u + run, s);
+    }
+    return;
   }
-  float s, inv;
-  am = group32_max(am);
-  choose_scale_mode<FMT>(am, smode, s, inv);
-  if (block * kBlock < d.numel && (threadIdx.x & 31) == 0) st_global<float>(d.scale + block, s);
+  for (int u = 0; u < kU; u++) {
+    const int64_t first = lo + u * kSubTile + run * kBlock;
+    float x[4], s;
 #pragma unroll
-  for (int j = 0; j < 4; j++) x[j] *= inv;
-  const uint32_t codes = encode4_nan<FMT>(x, nonfinite_amax(am));
+    for (int j = 0; j < 4; j++) x[j] = first + lane + 32 * j < d.numel ? ld_elem<DT>(d.x, first + lane + 32 * j) : 0.0f;
+    const uint32_t codes = block_to_codes<FMT>(x, smode, s);
+    if (first < d.numel && lane == 0) st_global<float>(d.scale + (first >> 7), s);
 #pragma unroll
-  for (int j = 0; j < 4; j++)
-    if (i0 + 32 * j < d.numel) st_global<uint8_t>(d.codes + i0 + 32 * j, (uint8_t)(codes >> (8 * j)));
+    for (int j = 0; j < 4; j++)
+      if (first + lane + 32 * j < d.numel)
+        st_global<uint8_t>(d.codes + first + lane + 32 * j, (uint8_t)(codes >> (8 * j)));
+  }
 }
 
-// Per-tensor scales, first pass: the amax of one chunk.
+// The largest |value| bits of two 16-bit values or of one in a dword, as fp32 bits.
+template <int DT>
+__device__ __forceinline__ uint32_t amax_word(uint32_t am, uint32_t x) {
+  if constexpr (DT == FP8ADAM_F32) return max(am, x & 0x7FFFFFFFu);
+  if constexpr (DT == FP8ADAM_BF16) return max(max(am, (x << 16) & 0x7FFF0000u), x & 0x7FFF0000u);
+  const f16x2 h = __builtin_bit_cast(f16x2, x);
+  return max(max(am, abs_bits((float)h[0])), abs_bits((float)h[1]));
+}
+
+// Per-tensor scales, first pass: the amax of one chunk, as sumsq_range reads it.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_quant_amax(const QuantDesc* __restrict__ descs,
                                                          const int32_t* __restrict__ chunk_tid,
                                                          uint32_t* __restrict__ amax) {
+  constexpr int kBytes = DT == FP8ADAM_F32 ? 4 : 2, kVec = 16 / kBytes;
   const int64_t w = blockIdx.x;
   const QuantDesc d = descs[chunk_tid[w]];
-  const int64_t lo = (w - d.chunk0) * d.chunk_len, hi = min(lo + d.chunk_len, d.numel);
+  const int64_t lo = (w - d.chunk0) * d.chunk_len, n = min(d.chunk_len, d.numel - lo);
+  const char* base = static_cast<const char*>(d.x) + kBytes * lo;
+  const int64_t head = min(n, (int64_t)((16u - ((uintptr_t)base & 15u)) & 15u) / kBytes);
+  const int64_t nvec = (n - head) / kVec, tail = head + nvec * kVec;
   uint32_t am = 0, none = 0;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) am = max(am, abs_bits(ld_elem<DT>(d.x, i)));
+  // a piece at a time, so that offsets into the buffer resource stay small
+  constexpr int64_t kPiece = (int64_t)1 << 20;
+  for (int64_t v0 = 0; v0 < nvec; v0 += kPiece) {
+    const int nv = (int)min(kPiece, nvec - v0);
+    const Rsrc r = rsrc(base + kBytes * head + 16 * v0, 16 * (int64_t)nv);
+    for (int v = threadIdx.x; v < nv; v += kThreads * kSumUnroll) {
+      vu4 x[kSumUnroll];
+#pragma unroll
+      for (int u = 0; u < kSumUnroll; u++)
+        x[u] = __builtin_amdgcn_raw_buffer_load_b128(r, 16 * (v + u * kThreads), 0, kLdPol);
+#pragma unroll
+      for (int u = 0; u < kSumUnroll; u++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) am = amax_word<DT>(am, x[u][j]);
+    }
+  }
+  const int64_t single = (int64_t)threadIdx.x < head ? (int64_t)threadIdx.x : tail + (int64_t)threadIdx.x - head;
+  if (single < n) am = max(am, abs_bits(ld_elem<DT>(base, single)));
   block_max2(am, none);
-  if (threadIdx.x == 0) amax[w] = am;
+  if (threadIdx.x == 0) amax[d.slot0 + (w - d.chunk0)] = am;
 }
 
-// Second pass: every work-group takes the largest of its tensor's chunk maxima
-// (at most kAmaxMaxChunks of them, from the L2), and quantizes its part.
+// Second pass: every wave takes the largest of its tensor's chunk maxima (at most
+// kAmaxMaxChunks of them, from the L2), and quantizes its share of the part.
 template <int DT, int FMT>
 __global__ __launch_bounds__(kThreads) void k_quant_tensor(const QuantDesc* __restrict__ descs,
                                                            const int32_t* __restrict__ part_tid, int64_t nparts,
                                                            const uint32_t* __restrict__ amax, int smode) {
-  const int64_t w = work_index<kXcdStreams>(nparts);
+  constexpr int64_t kLen = (int64_t)1 << kQuantTensorPartLog2;
+  constexpr int kU = (int)(kLen / kSubTile);
+  const int64_t w = run_index(nparts);
   if (w < 0) return;
   const QuantDesc d = descs[part_tid[w]];
-  uint32_t am = 0;
-  for (int64_t k = threadIdx.x & 63; k < d.nchunks; k += 64) am = max(am, amax[d.chunk0 + k]);
+  const int64_t lo = d.head + ((w - d.part0) << kQuantTensorPartLog2);
+  const bool whole = d.vec && lo + kLen <= d.numel;
+  // the maxima first, then the values: the scale is ready when they arrive
+  const vu4 maxima = __builtin_amdgcn_raw_buffer_load_b128(rsrc(amax + d.slot0, 4 * d.slots), 16 * (threadIdx.x & 63), 0, 0);
+  Raw4<DT> r[kU];
+  if (whole) {
+    const Rsrc bx = typed_rsrc<DT>(d.x, lo, kLen);
+#pragma unroll
+    for (int u = 0; u < kU; u++) r[u] = load4<DT>(bx, 4 * threadIdx.x + u * kSubTile);
+  }
+  const uint32_t am = wave_max(max(max(maxima.x, maxima.y), max(maxima.z, maxima.w)));
   float s, inv;
-  am = wave_max(am);
   choose_scale_mode<FMT>(am, smode, s, inv);
-  if (w == d.part0 && threadIdx.x == 0) st_global<float>(d.scale, s);
-  const int64_t lo = (w - d.part0) << kQuantTensorPartLog2;
-  const int64_t hi = min(lo + ((int64_t)1 << kQuantTensorPartLog2), d.numel);
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+  const bool odd = nonfinite_amax(am);
+  if (whole) {
+    const Rsrc bc = rsrc(d.codes + lo, kLen);
+#pragma unroll
+    for (int u = 0; u < kU; u++) {
+      float x[4];
+      unpack4<DT>(r[u], x);
+#pragma unroll
+      for (int j = 0; j < 4; j++) x[j] *= inv;
+      __builtin_amdgcn_raw_buffer_store_b32(encode4_nan<FMT>(x, odd), bc, 4 * threadIdx.x + u * kSubTile, 0, kStPol);
+    }
+  }
+  const bool first = w == d.part0;
+  if (first && threadIdx.x == 0) st_global<float>(d.scale, s);
+  // what is not in groups: all of another part, and the elements in front of the first
+  const int64_t from = first ? 0 : lo, to = whole ? first ? (int64_t)d.head : lo : min(lo + kLen, d.numel);
+  for (int64_t i = from + threadIdx.x; i < to; i += kThreads) {
     const float x[4] = {ld_elem<DT>(d.x, i) * inv, 0.0f, 0.0f, 0.0f};
-    st_global<uint8_t>(d.codes + i, (uint8_t)encode4_nan<FMT>(x, nonfinite_amax(am)));
+    st_global<uint8_t>(d.codes + i, (uint8_t)encode4_nan<FMT>(x, odd));
   }
 }
 
 template <int DT, int FMT, bool BLK>
 __global__ __launch_bounds__(kThreads) void k_dequant(const QuantDesc* __restrict__ descs,
-                                                      const int32_t* __restrict__ part_tid, int64_t nparts,
-                                                      int part_log2) {
-  const int64_t w = work_index<kXcdStreams>(nparts);
+                                                      const int32_t* __restrict__ part_tid, int64_t nparts) {
+  constexpr int PL = BLK ? kQuantPartLog2 : kQuantTensorPartLog2;
+  constexpr int64_t kLen = (int64_t)1 << PL;
+  constexpr int kU = (int)(kLen / kSubTile);
+  const int64_t w = run_index(nparts);
   if (w < 0) return;
   const QuantDesc d = descs[part_tid[w]];
-  const int64_t lo = (w - d.part0) << part_log2;
-  const int64_t hi = min(lo + ((int64_t)1 << part_log2), d.numel);
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads)
+  const int64_t lo = d.head + ((w - d.part0) << PL);
+  const bool whole = d.vec && lo + kLen <= d.numel, first = w == d.part0;
+  if (whole) {
+    const Rsrc bx = typed_rsrc<DT>(d.x, lo, kLen), bc = rsrc(d.codes + lo, kLen);
+    uint32_t c[kU];
+    float s[kU];
+#pragma unroll
+    for (int u = 0; u < kU; u++) {
+      c[u] = __builtin_amdgcn_raw_buffer_load_b32(bc, 4 * threadIdx.x + u * kSubTile, 0, kLdPol);
+      s[u] = ld_global<float>(d.scale + (BLK ? (lo >> 7) + 8 * u + (threadIdx.x >> 5) : 0));
+    }
+#pragma unroll
+    for (int u = 0; u < kU; u++) {
+      float x[4];
+      decode4<FMT>(c[u], x);
+#pragma unroll
+      for (int j = 0; j < 4; j++) x[j] *= s[u];
+      store4<DT>(bx, 4 * threadIdx.x + u * kSubTile, x);
+    }
+  }
+  const int64_t from = first ? 0 : lo, to = whole ? first ? (int64_t)d.head : lo : min(lo + kLen, d.numel);
+  for (int64_t i = from + threadIdx.x; i < to; i += kThreads)
     st_elem<DT>(d.x, i, decode1<FMT>(ld_global<uint8_t>(d.codes + i)) * ld_global<float>(d.scale + (BLK ? i >> 7 : 0)));
 }
 
@@ -356,7 +465,6 @@ struct Span {
   std::vector<int32_t> ctid; // amax chunk -> tensor
   const int32_t* d_ctid = nullptr;
   int64_t nchunks = 0;
-  int64_t chunk_base = 0;    // the kind's first amax chunk in the plan's array
 };
 
 bool valid_dtype(int32_t d) { return d >= FP8ADAM_F32 && d <= FP8ADAM_F16; }
@@ -364,7 +472,7 @@ bool valid_format(int32_t f) { return f == FP8ADAM_E4M3 || f == FP8ADAM_E5M2; }
 
 // Elements of one plan: every launch has to fit one grid dimension (2^32 - 1
 // work-items of work-groups of 1024 elements).
-constexpr int64_t kMaxGroupsPerLaunch = ((int64_t)UINT32_MAX / kThreads) & ~(int64_t)7;
+constexpr int64_t kMaxGroupsPerLaunch = ((int64_t)UINT32_MAX / kThreads) / (8 * kXcdRun) * (8 * kXcdRun);
 
 std::string of_tensor(const char* what, int32_t t) { return std::string(what) + " of tensor " + std::to_string(t); }
 
@@ -556,14 +664,13 @@ void group_consts(const fp8adam_adamw_hparams* h, int n_groups, int64_t t, Adamw
 template <int DT, int FMT>
 int run_quantize(fp8adam_plan* p, const Span& k, hipStream_t s) {
   const QuantDesc* d = static_cast<const QuantDesc*>(p->d_desc);
-  const dim3 grid(grid_for<kXcdStreams>(k.nparts));
+  const dim3 grid(run_grid(k.nparts));
   if (p->granularity == FP8ADAM_SCALE_BLOCK128) {
     hipLaunchKernelGGL((k_quant_block<DT, FMT>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts, p->smode);
   } else {
-    uint32_t* amax = p->d_amax + k.chunk_base;
-    hipLaunchKernelGGL((k_quant_amax<DT>), dim3((unsigned)k.nchunks), dim3(kThreads), 0, s, d, k.d_ctid, amax);
+    hipLaunchKernelGGL((k_quant_amax<DT>), dim3((unsigned)k.nchunks), dim3(kThreads), 0, s, d, k.d_ctid, p->d_amax);
     HIP_TRY(hipGetLastError());
-    hipLaunchKernelGGL((k_quant_tensor<DT, FMT>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts, amax, p->smode);
+    hipLaunchKernelGGL((k_quant_tensor<DT, FMT>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts, p->d_amax, p->smode);
   }
   HIP_TRY(hipGetLastError());
   return 0;
@@ -572,12 +679,11 @@ int run_quantize(fp8adam_plan* p, const Span& k, hipStream_t s) {
 template <int DT, int FMT>
 int run_dequantize(fp8adam_plan* p, const Span& k, hipStream_t s) {
   const QuantDesc* d = static_cast<const QuantDesc*>(p->d_desc);
-  const dim3 grid(grid_for<kXcdStreams>(k.nparts));
+  const dim3 grid(run_grid(k.nparts));
   if (p->granularity == FP8ADAM_SCALE_BLOCK128)
-    hipLaunchKernelGGL((k_dequant<DT, FMT, true>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts, kQuantPartLog2);
+    hipLaunchKernelGGL((k_dequant<DT, FMT, true>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts);
   else
-    hipLaunchKernelGGL((k_dequant<DT, FMT, false>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts,
-                       kQuantTensorPartLog2);
+    hipLaunchKernelGGL((k_dequant<DT, FMT, false>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts);
   HIP_TRY(hipGetLastError());
   return 0;
 }
@@ -783,11 +889,19 @@ int quant_plan(fp8adam_plan** out, const fp8adam_quant_tensor* T, int32_t n, con
   p->smode = cfg->scale_mode;
   const int pl = block ? kQuantPartLog2 : kQuantTensorPartLog2;
   std::vector<QuantDesc> desc((size_t)n);
+  int64_t slots = 0;
   for (int32_t t = 0; t < n; t++) {
     const fp8adam_quant_tensor& x = T[t];
     QuantDesc& d = desc[t];
-    d = QuantDesc{x.values, x.codes, x.scale, x.numel, 0, 0, 0, 0};
+    d = QuantDesc{x.values, x.codes, x.scale, x.numel, 0, 0, 0, 0, 0, 0, 0};
     if (x.numel == 0) continue;
+    // the first element from which values and codes both lie on dwords (blocks start at element 0)
+    const bool wide = x.dtype == FP8ADAM_F32;
+    for (int h = 0; h < (block ? 1 : 4) && !d.vec; h++)
+      if ((((uintptr_t)x.codes + h) & 3u) == 0 && (wide || (((uintptr_t)x.values + 2 * h) & 3u) == 0)) {
+        d.head = h;
+        d.vec = 1;
+      }
     auto it = std::find_if(p->spans.begin(), p->spans.end(),
                            [&](const Span& k) { return k.dtype == x.dtype && k.format == x.format; });
     if (it == p->spans.end()) {
@@ -797,29 +911,30 @@ int quant_plan(fp8adam_plan** out, const fp8adam_quant_tensor* T, int32_t n, con
       it->format = x.format;
     }
     d.part0 = (int64_t)it->tid.size();
-    const int64_t parts = (x.numel + ((int64_t)1 << pl) - 1) >> pl;
+    const int64_t parts = std::max<int64_t>(1, (x.numel - d.head + ((int64_t)1 << pl) - 1) >> pl);
     if (int r = check_parts(d.part0 + parts)) return r;
     it->tid.insert(it->tid.end(), (size_t)parts, t);
     if (!block) {
       d.chunk0 = (int64_t)it->ctid.size();
       const int64_t len = (x.numel + kAmaxMaxChunks - 1) / kAmaxMaxChunks;
       d.chunk_len = (len + kAmaxMinChunk - 1) / kAmaxMinChunk * kAmaxMinChunk;
-      d.nchunks = (x.numel + d.chunk_len - 1) / d.chunk_len;
-      it->ctid.insert(it->ctid.end(), (size_t)d.nchunks, t);
+      const int64_t nc = (x.numel + d.chunk_len - 1) / d.chunk_len;
+      it->ctid.insert(it->ctid.end(), (size_t)nc, t);
+      d.slot0 = slots;
+      d.slots = (int32_t)((nc + 3) & ~(int64_t)3);
+      slots += d.slots;
     }
   }
   if (int r = plan_device(p, stream)) return r;
   Image im;
   const size_t at_desc = im.put(desc.data(), sizeof(QuantDesc) * desc.size());
   std::vector<size_t> at, atc;
-  int64_t chunks = 0;
   for (Span& k : p->spans) {
     at.push_back(im.put(k.tid.data(), sizeof(int32_t) * k.tid.size()));
     atc.push_back(im.put(k.ctid.data(), sizeof(int32_t) * k.ctid.size()));
-    k.chunk_base = chunks;
-    chunks += (int64_t)k.ctid.size();
   }
-  const size_t at_amax = im.room(sizeof(uint32_t) * (size_t)chunks);
+  const std::vector<uint32_t> zeros((size_t)slots, 0u);
+  const size_t at_amax = im.put(zeros.data(), sizeof(uint32_t) * zeros.size());
   if (int r = im.upload(p, stream)) return r;
   p->d_desc = p->mem + at_desc;
   p->d_amax = reinterpret_cast<uint32_t*>(p->mem + at_amax);
