@@ -168,7 +168,7 @@ __global__ __launch_bounds__(kReduceThreads) void k_gradctl(const double* __rest
   if (threadIdx.x != 0) return;
   float gfac;
   int64_t t;
-  if (!scaler_decide(st, cfg, sacc[0], sbad[0] > 0.0, gfac, t)) {
+  if (!scaler_decide(st, load_scaler(st), cfg, sacc[0], sbad[0] > 0.0, gfac, t)) {
     st_global(&ctl->skip, 1);
     return;
   }

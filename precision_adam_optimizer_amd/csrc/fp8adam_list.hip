@@ -135,7 +135,8 @@ __device__ __forceinline__ double total_of(const double* __restrict__ partial, i
 }
 
 // Loss scaling: the scaler's decision, and each group's bias corrections at the
-// device-side t.
+// device-side t (of the step about to be taken; of no use to a skipped one).  What
+// does not need the sum is done before it.
 struct GroupRates {
   double lr[FP8ADAM_MAX_GROUPS], beta1[FP8ADAM_MAX_GROUPS], beta2[FP8ADAM_MAX_GROUPS];
 };
@@ -143,22 +144,20 @@ struct GroupRates {
 __global__ __launch_bounds__(kThreads) void k_list_ctl(const double* __restrict__ partial, int npartial,
                                                        fp8adam_amp_state* __restrict__ st, AdamwCtl* __restrict__ ctl,
                                                        fp8adam_amp_config cfg, GroupRates R, int n_groups) {
-  const double sumsq = total_of(partial, npartial);
-  __shared__ int64_t t_now;
-  if (threadIdx.x == 0) {
-    float gfac = 0.0f;
-    int64_t t = 0;
-    const bool run = scaler_decide(st, cfg, sumsq, !isfinite(sumsq), gfac, t);
-    ctl->skip = run ? 0 : 1;
-    ctl->gfac = gfac;
-    t_now = t;
-  }
-  __syncthreads();
+  const ScalerState was = load_scaler(st);
   const int q = threadIdx.x;
-  if (q < n_groups && t_now > 0) {
-    ctl->step_size[q] = (float)(R.lr[q] / (1.0 - pow(R.beta1[q], (double)t_now)));
-    ctl->inv_bc2[q] = (float)(1.0 / (1.0 - pow(R.beta2[q], (double)t_now)));
+  if (q < n_groups) {
+    const double t = (double)(was.step + 1);
+    ctl->step_size[q] = (float)(R.lr[q] / (1.0 - pow(R.beta1[q], t)));
+    ctl->inv_bc2[q] = (float)(1.0 / (1.0 - pow(R.beta2[q], t)));
   }
+  const double sumsq = total_of(partial, npartial);
+  if (threadIdx.x != 0) return;
+  float gfac = 0.0f;
+  int64_t t = 0;
+  const bool run = scaler_decide(st, was, cfg, sumsq, !isfinite(sumsq), gfac, t);
+  ctl->skip = run ? 0 : 1;
+  ctl->gfac = gfac;
 }
 
 constexpr int kClipUnroll = 4;
@@ -642,6 +641,10 @@ int check_groups(const fp8adam_plan* p, const fp8adam_adamw_hparams* h, int32_t 
     if (!(h[q].eps >= 0.0) || !isfinite(h[q].eps)) return fail(FP8ADAM_EINVAL, "eps must be finite and >= 0");
     if (!isfinite(h[q].lr) || !isfinite(h[q].weight_decay))
       return fail(FP8ADAM_EINVAL, "lr and weight_decay must be finite");
+    // what the kernels take of them in fp32 (1 / (1 - beta) bounds the bias corrections)
+    if (!isfinite((float)(h[q].lr / (1.0 - h[q].beta1))) || !isfinite((float)(h[q].lr * h[q].weight_decay)) ||
+        !isfinite((float)h[q].eps) || !isfinite((float)(1.0 / (1.0 - h[q].beta2))))
+      return fail(FP8ADAM_EINVAL, "lr, lr * weight_decay, lr / (1 - beta1), 1 / (1 - beta2) and eps must be finite in fp32");
   }
   return 0;
 }

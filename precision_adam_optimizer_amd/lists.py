@@ -69,8 +69,9 @@ def _lib() -> ctypes.CDLL:
         L.fp8adam_plan_destroy.argtypes = [vp]
         L.fp8adam_plan_destroy.restype = None
         L.fp8adam_adamw_plan.argtypes = [P(vp), P(AdamwTensorArg), i32, P(AdamwConfigArg), vp]
-        L.fp8adam_adamw_step.argtypes = [vp, P(AdamwHParamsArg), i32, i64, vp]
-        L.fp8adam_adamw_step_amp.argtypes = [vp, P(AdamwHParamsArg), i32, P(AmpConfigArg), vp, vp]
+        # the hyperparameters by address, which the classes below keep: a call's pointer costs a small step 0.5 us
+        L.fp8adam_adamw_step.argtypes = [vp, vp, i32, i64, vp]
+        L.fp8adam_adamw_step_amp.argtypes = [vp, vp, i32, P(AmpConfigArg), vp, vp]
         L.fp8adam_clip_plan.argtypes = [P(vp), P(ClipTensorArg), i32, vp]
         L.fp8adam_clip_grads.argtypes = [vp, ctypes.c_float, vp, vp]
         L.fp8adam_quant_plan.argtypes = [P(vp), P(QuantTensorArg), i32, P(QuantConfigArg), vp]
@@ -169,9 +170,10 @@ def _need(ok: bool, i: int, what: str) -> None:
         raise ValueError(f"tensor {i}: {what}")
 
 
-def _check_flat(t: torch.Tensor, i: int, what: str, dtypes, numel: int) -> None:
-    _need(t.dtype in dtypes, i, f"{what} must be {' or '.join(str(d).replace('torch.', '') for d in dtypes)}")
-    _need(t.numel() == numel, i, f"{what} must have {numel} elements")
+def _check_flat(t: torch.Tensor, i: int, what: str, dtype, numel: int, at_least: bool = False) -> None:
+    _need(t.dtype == dtype, i, f"{what} must be {str(dtype).replace('torch.', '')}")
+    _need(t.numel() == numel or (at_least and t.numel() > numel), i,
+          f"{what} must have {'at least ' if at_least else ''}{numel} elements")
     _need(t.is_contiguous(), i, f"{what} must be contiguous")
 
 
@@ -275,7 +277,7 @@ class AdamW(_Planned):
                 return torch.zeros_like(p, dtype=torch.float32) if b == 32 else p.new_zeros(p.numel(), dtype=torch.uint8)
 
             def ones(p, b):
-                return None if b == 32 else p.new_ones(_blocks(p.numel()), dtype=torch.float32)
+                return None if b == 32 else p.new_ones(max(1, _blocks(p.numel())), dtype=torch.float32)
             state = [[zeros(p, b) for p, b in zip(params, bits)] for _ in range(2)]
             state += [[ones(p, b) for p, b in zip(params, bits)] for _ in range(2)]
         state = [list(x) for x in state]
@@ -291,9 +293,9 @@ class AdamW(_Planned):
                         t.is_contiguous() and t.dim() == 1 and t.numel() == p.numel())), i,
                           f"32-bit moments ({what}) must be float32 of the weight's size and order in memory")
                 else:
-                    _check_flat(t, i, f"8-bit moments ({what})", (torch.uint8,), p.numel())
+                    _check_flat(t, i, f"8-bit moments ({what})", torch.uint8, p.numel())
                     _need(s is not None, i, f"8-bit moments ({what}) need scales")
-                    _check_flat(s, i, f"scales of 8-bit moments ({what})", (torch.float32,), _blocks(p.numel()))
+                    _check_flat(s, i, f"scales of 8-bit moments ({what})", torch.float32, _blocks(p.numel()), True)
         dev = _one_gpu([t for x in (params, grads, copies, *state) for t in x if t is not None])
         self.params, self.grads, self.copies, self.groups, self.state_bits = params, grads, copies, groups, bits
         args = [AdamwTensorArg(_ptr(p), _ptr(g), _ptr(c), _ptr(m), _ptr(v), _ptr(ms) if b == 8 else None,
@@ -303,10 +305,18 @@ class AdamW(_Planned):
         self.formats = (m_format, v_format)
         cfg = AdamwConfigArg(self.n_groups, _FORMATS[m_format], _FORMATS[v_format], 0)
         self._hp = (AdamwHParamsArg * self.n_groups)()
+        self._hp_at = ctypes.addressof(self._hp)
+        self._given = None
         self._build(dev, lambda: fp8adam_adamw_plan(args, cfg))
 
-    def _set(self, **hyper) -> None:
-        for name, x in hyper.items():
+    def _set(self, lr, beta1, beta2, eps, weight_decay) -> None:
+        """The groups' hyperparameters into the array that the calls pass (left as it is where
+        they are those of the call before)."""
+        given = (lr, beta1, beta2, eps, weight_decay)
+        if given == self._given:
+            return
+        self._given = None
+        for name, x in zip(("lr", "beta1", "beta2", "eps", "weight_decay"), given):
             if isinstance(x, (list, tuple)):
                 if len(x) != self.n_groups:
                     raise ValueError(f"{name} must be a number or one for each of the {self.n_groups} groups")
@@ -315,11 +325,14 @@ class AdamW(_Planned):
             else:
                 for h in self._hp:
                     setattr(h, name, x)
+        flat = [y for x in given for y in (x if type(x) is tuple else (x,))]
+        if all(type(y) in (float, int) for y in flat):  # (a list or a tensor could change in place)
+            self._given = given
 
     def step(self, *, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step: int) -> None:
         """One step; ``step`` is the 1-based t of the bias corrections."""
-        self._set(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay)
-        self._call(_lib().fp8adam_adamw_step, self._hp, self.n_groups, step)
+        self._set(lr, beta1, beta2, eps, weight_decay)
+        self._call(_lib().fp8adam_adamw_step, self._hp_at, self.n_groups, step)
 
     def step_amp(self, amp_state: torch.Tensor, *, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0,
                  max_norm: float = 0.0, growth_factor: float = 2.0, backoff_factor: float = 0.5,
@@ -331,9 +344,9 @@ class AdamW(_Planned):
             raise ValueError("amp_state must be the 32-byte tensor from amp_state()")
         if amp_state.device != self.device or not amp_state.is_contiguous():
             raise ValueError("amp_state must be contiguous and on the weights' device")
-        self._set(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay)
+        self._set(lr, beta1, beta2, eps, weight_decay)
         amp = AmpConfigArg(max_norm, growth_factor, backoff_factor, growth_interval)
-        self._call(_lib().fp8adam_adamw_step_amp, self._hp, self.n_groups, ctypes.byref(amp), amp_state.data_ptr())
+        self._call(_lib().fp8adam_adamw_step_amp, self._hp_at, self.n_groups, ctypes.byref(amp), amp_state.data_ptr())
 
     def checkpoint(self) -> list:
         """Copies of the moments in the form ``state=`` takes: [m, v, m_scale, v_scale].
@@ -391,12 +404,13 @@ class GradClip(_Planned):
         args = [ClipTensorArg(_ptr(g), _ptr(o), g.numel(), _DTYPES[g.dtype], 0 if o is None else _DTYPES[o.dtype])
                 for g, o in zip(grads, outs)]
         self.result = torch.zeros(2, dtype=torch.float32, device=dev)
+        self._result_at = self.result.data_ptr()
         self._build(dev, lambda: fp8adam_clip_plan(args))
 
     def clip(self, max_norm: float) -> torch.Tensor:
         """Clips to max_norm (0 or less: no limit) and returns (norm, coefficient): a tensor on the
         device that the next call overwrites."""
-        self._call(_lib().fp8adam_clip_grads, max_norm, self.result.data_ptr())
+        self._call(_lib().fp8adam_clip_grads, max_norm, self._result_at)
         return self.result
 
 
@@ -407,7 +421,7 @@ class Quantizer(_Planned):
     memory).  ``fmt``: "e4m3" or "e5m2", for the list or one for each tensor.
     ``granularity``: one scale per 128 elements ("block128") or per tensor ("tensor");
     ``scale_mode`` "pow2" or "amax", as for the step.  ``codes`` (uint8, one per element)
-    and ``scales`` (float32, ceil(numel / 128) or 1 each) are allocated unless given.
+    and ``scales`` (float32, at least ceil(numel / 128) or 1 each) are allocated unless given.
     """
 
     def __init__(self, values, *, fmt="e4m3", granularity="block128", scale_mode="pow2", codes=None, scales=None):
@@ -423,15 +437,16 @@ class Quantizer(_Planned):
         if codes is None:
             codes = [x.new_empty(x.numel(), dtype=torch.uint8) for x in values]
         if scales is None:
-            scales = [x.new_ones(count(x), dtype=torch.float32) for x in values]
+            # (one, unused, for an empty tensor too, as in FP8AdamW's state)
+            scales = [x.new_ones(max(1, count(x)), dtype=torch.float32) for x in values]
         codes, scales = list(codes), list(scales)
         if not len(fmts) == len(codes) == len(scales) == n:
             raise ValueError("fmt, codes and scales need one entry per tensor")
         for i, (x, c, s) in enumerate(zip(values, codes, scales)):
             _need(x.dtype in _DTYPES, i, "values must be float32, bfloat16 or float16")
             _need(_dense(x), i, "values must be dense")
-            _check_flat(c, i, "codes", (torch.uint8,), x.numel())
-            _check_flat(s, i, "scales", (torch.float32,), count(x))
+            _check_flat(c, i, "codes", torch.uint8, x.numel())
+            _check_flat(s, i, "scales", torch.float32, count(x), True)
         dev = _one_gpu(values + codes + scales)
         self.values, self.codes, self.scales = values, codes, scales
         args = [QuantTensorArg(_ptr(x), _ptr(c), _ptr(s), x.numel(), _DTYPES[x.dtype], _FORMATS[f])

@@ -228,7 +228,7 @@ def test_adamw_mixed_list_and_groups():
             c.check()
     with pytest.raises(ValueError, match="each of the 3 groups"):
         opt.step(step=7, **{**hp, "lr": [1e-3]})
-    for bad in (dict(lr=math.inf), dict(beta1=1.0), dict(beta2=-0.1), dict(eps=-1.0), dict(weight_decay=math.nan)):
+    for bad in (dict(lr=math.inf), dict(lr=1e39), dict(eps=1e39), dict(lr=1e30, weight_decay=1e30), dict(beta1=1.0), dict(beta2=-0.1), dict(eps=-1.0), dict(weight_decay=math.nan)):
         with pytest.raises(pk.Fp8AdamError):
             opt.step(step=7, **{**hp, **bad})
     with pytest.raises(pk.Fp8AdamError, match="step"):
@@ -558,14 +558,14 @@ def test_quantize_mixed_list_nonfinite_and_extremes():
 def test_state_goes_between_32_and_8_bits():
     """32-bit moments to both kinds of FP8AdamW state and to AdamW's 8-bit one, and back."""
     g = gen(10)
-    cases = [Case(n, g) for n in SIZES if n]
+    cases = [Case(n, g) for n in SIZES]
     opt = optimizer(cases)
     opt.step(step=1, **HP)
     eight = opt.converted_state(8)
     for k, c in enumerate(cases):
         for j, (x, fmt) in enumerate(((c.m, "e4m3"), (c.v, "e5m2"))):
             codes, s = quantized(x.cpu(), fmt)
-            assert torch.equal(eight[j][k].cpu(), codes) and torch.equal(eight[2 + j][k].cpu(), s)
+            assert torch.equal(eight[j][k].cpu(), codes) and (c.n == 0 or torch.equal(eight[2 + j][k].cpu(), s))
     p, gr = [c.p.clone() for c in cases], [c.g.clone() for c in cases]
     opt8 = pk.AdamW(p, gr, state_bits=8, state=eight)
     back = opt8.converted_state(32)
