@@ -31,15 +31,24 @@ using namespace fp8adam_engine;
 // 64 are 2 to 6% slower on the largest.  A surplus work-group gets -1.
 constexpr int64_t kXcdRun = 32;
 
+template <int64_t RUN = kXcdRun>
 __device__ __forceinline__ int64_t run_index(int64_t nparts) {
   const int64_t xcd = blockIdx.x & 7u, k = blockIdx.x >> 3;
-  const int64_t w = (k / kXcdRun) * (8 * kXcdRun) + xcd * kXcdRun + k % kXcdRun;
+  const int64_t w = (k / RUN) * (8 * RUN) + xcd * RUN + k % RUN;
   return w < nparts ? w : -1;
 }
 
+template <int64_t RUN = kXcdRun>
 inline unsigned run_grid(int64_t nparts) {
-  return (unsigned)((nparts + 8 * kXcdRun - 1) / (8 * kXcdRun) * (8 * kXcdRun));
+  return (unsigned)((nparts + 8 * RUN - 1) / (8 * RUN) * (8 * RUN));
 }
+
+// Shared memory that a launch reserves, and does not use, so that at most `groups`
+// of its work-groups share a CU (8 do without).  Where most of the traffic is
+// writes, fewer of them in flight reach HBM faster; each launch that does this says
+// what it gains.
+constexpr unsigned kCuLds = 160 * 1024;
+constexpr unsigned lds_for(int groups) { return groups >= 8 ? 0u : kCuLds / (groups + 1) + 1024u; }
 
 // --------------------------------------------------------------- typed elements
 
@@ -196,7 +205,11 @@ __device__ __forceinline__ float adamw_element(const GroupConsts& c, float g, fl
   return p - __builtin_fmaf(c.lr_wd, p, upd);
 }
 
-// log2 of a part's elements: 256 lanes of 4, twice where an element moves few bytes.
+// log2 of a part's elements: 256 lanes of 4, twice where an element moves few bytes
+// (8-bit moments of 16-bit weights).  842M fp32 weights with 32-bit moments: 1024
+// elements 4.15 ms, 2048 4.24, 4096 4.35; 109.5M with 8-bit moments, scaled and
+// clipped: 1024 320 us, 2048 330; 842M bf16 weights with 8-bit moments: 1024 1.37
+// ms, 2048 1.36, 4096 1.44.
 constexpr int adamw_part_log2(int pd, bool s8) { return s8 && pd != FP8ADAM_F32 ? 11 : 10; }
 
 // The moments of a run of 128 elements that 32 lanes own, four each: new scales
@@ -226,6 +239,17 @@ __device__ __forceinline__ void moments_to_codes(const float (&m1)[4], const flo
 // groups of four consecutive elements per lane, through buffer resources; another
 // one element by element, where lane h of the 32 holds elements h, h + 32, h + 64
 // and h + 96 of its run, so that accesses are contiguous at any alignment.
+//
+// Bound by HBM, each stream read and written once (counters: 14.0 bytes fetched and
+// 14.0 written per fp32 weight with a bf16 gradient, a bf16 copy and 32-bit
+// moments).  842M of those take 4.0 ms, 5.95 TB/s: a little over what a 1:1 copy
+// reaches on the card (5.86), and 92% of reads and writes one after the other at
+// their own rates.
+// 842M bf16 weights with bf16 gradients and 8-bit moments (10.1 bytes): 1.35 ms,
+// 6.3 TB/s, 95% of that bound.  The smallest lists are bound by the launch: 65
+// tensors of 4096 take 3 us on the device, 5.7 us with the call.  Packed fp32
+// tensors of odd sizes cost no more (every fp32 stream starts on a dword): 7M
+// weights in 48 of them 35 us, 5.7 TB/s.
 template <int PD, int CD, int GD, bool S8, int MF, int VF>
 __global__ __launch_bounds__(kThreads) void k_adamw(const AdamwDesc* __restrict__ descs,
                                                     const int32_t* __restrict__ part_tid, AdamwConsts C, int64_t nparts,
@@ -387,8 +411,11 @@ struct AdamwKind {
 template <int PD, int CD, int GD, bool S8, int MF, int VF>
 inline void launch_adamw_kind(const AdamwDesc* descs, const int32_t* part_tid, const AdamwConsts& C, int64_t nparts,
                               const AdamwCtl* ctl, hipStream_t s) {
-  hipLaunchKernelGGL((k_adamw<PD, CD, GD, S8, MF, VF>), dim3(run_grid(nparts)), dim3(kThreads), 0, s, descs,
-                     part_tid, C, nparts, ctl);
+  // 32-bit moments: five work-groups on a CU.  842M fp32 weights with a copy 3.96 ms against 4.09 with
+  // eight (four: 3.98, three: 4.03), without one 3.59 against 3.73; 109.5M with a copy 507 us against 519
+  // (four: 525); 842M bf16 weights 3.04 ms against 3.06.  8-bit moments read more than they write: they lose.
+  hipLaunchKernelGGL((k_adamw<PD, CD, GD, S8, MF, VF>), dim3(run_grid(nparts)), dim3(kThreads), lds_for(S8 ? 8 : 5), s,
+                     descs, part_tid, C, nparts, ctl);
 }
 
 // The launch of one kind's parts (the caller checks the launch).

@@ -682,6 +682,98 @@ def test_streams_and_graph_replays():
             o.close()
 
 
+def ragged(total, count, g):
+    """Sizes of `count` tensors, many of them empty or tiny, that fill `total` elements."""
+    cuts = torch.randint(0, total + 1, (count - 1,), generator=g, device="cuda").sort().values.tolist()
+    cuts = [0] + cuts + [total]
+    cuts[3:6] = [cuts[3]] * 3  # some empty ones
+    return list(zip(cuts[:-1], cuts[1:]))
+
+
+@pytest.mark.parametrize("pd, gd", [(F32, F32), (BF16, BF16), (F16, BF16)])
+def test_a_list_of_thousands_equals_one_tensor(pd, gd):
+    """What is elementwise does not see where one tensor ends: a packed list of 3000 ragged views
+    (any alignment) gives the bits of the one tensor they lie in."""
+    g = gen(14)
+    n = 300007
+    p, gr = filled(n, pd, g, 0.02), filled(n, gd, g, 1e-3)
+    m, v = torch.randn(n, generator=g, device="cuda") * 1e-4, torch.rand(n, generator=g, device="cuda") * 1e-6
+    spans = ragged(n, 3000, g)
+    one, many = [[x.clone() for x in (p, m, v)] for _ in range(2)]
+    a = pk.AdamW([one[0]], [gr], state=([one[1]], [one[2]]))
+    b = pk.AdamW([many[0][i:j] for i, j in spans], [gr[i:j] for i, j in spans],
+                 state=([many[1][i:j] for i, j in spans], [many[2][i:j] for i, j in spans]))
+    for t in (1, 2):
+        a.step(step=t, **HP)
+        b.step(step=t, **HP)
+    assert all(torch.equal(x, y) for x, y in zip(one, many))
+    out1, out2 = torch.zeros(n, device="cuda", dtype=BF16), torch.zeros(n, device="cuda", dtype=BF16)
+    c1 = pk.GradClip([gr], outs=[out1])
+    c2 = pk.GradClip([gr[i:j] for i, j in spans], outs=[out2[i:j] for i, j in spans])
+    r1, r2 = c1.clip(0.1).clone(), c2.clip(0.1).clone()
+    # the partial sums differ, in fp64: the norm by at most its rounding to fp32
+    assert abs(float(r1[0]) - float(r2[0])) <= 2 * U * float(r1[0])
+    if torch.equal(r1, r2):
+        assert torch.equal(out1, out2)
+    for o in (a, b, c1, c2):
+        o.close()
+
+
+def test_amp_over_every_kind_in_one_list():
+    """One norm over gradients of three types, then every kind of tensor with the same factor."""
+    g = gen(15)
+    S = 512.0
+    cases = [Case(n, g, pd, gd, cd, bits, offset=k % 2, gscale=1e-2 * S)
+             for k, (pd, cd) in enumerate(WEIGHTS) for gd in (F32, BF16, F16) for bits in (32, 8) for n in (900, 5)]
+    opt = optimizer(cases)
+    amp = pk.amp_state(S)
+    for t in (1, 2):
+        norm = math.sqrt(sum(float(c.g.double().square().sum()) for c in cases)) / S
+        factor = f32(f32(min(1.0, 0.3 / (norm + 1e-6))) * f32(1 / S))
+        for c in cases:
+            c.expect(t, **HP, factor=factor)
+        opt.step_amp(amp, max_norm=0.3, **HP)
+        assert amp_fields(amp)["grad_factor"] == factor
+        for c in cases:
+            c.check()
+    opt.close()
+
+
+def test_two_plans_at_once():
+    """Calls of different plans on two streams do not touch each other's workspace."""
+    def make(seed):
+        g = gen(seed)
+        cases = [Case(200003, g, bits=b, gscale=3.0) for b in (32, 8)]
+        half = [torch.zeros(c.n, device="cuda", dtype=BF16) for c in cases]
+        return cases, optimizer(cases), pk.GradClip([c.g for c in cases], outs=half), half, \
+            pk.Quantizer([c.p for c in cases], granularity="tensor"), pk.amp_state(8.0)
+
+    def run(x):
+        for _ in range(5):
+            x[2].clip(1.0)
+            x[1].step_amp(x[5], max_norm=1.0, **HP)
+            x[4].quantize()
+
+    def values(x):
+        return [t.clone() for t in x[3] + x[4].codes + x[4].scales + [x[2].result, x[5]] + [y for c in x[0] for y in (c.p, c.m, c.v)]]
+
+    a, b = make(16), make(17)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for x, st in zip((a, b), streams):
+        with torch.cuda.stream(st):
+            run(x)
+    torch.cuda.synchronize()
+    for x, seed in ((a, 16), (b, 17)):
+        y = make(seed)
+        run(y)
+        torch.cuda.synchronize()
+        assert all(torch.equal(i, j) for i, j in zip(values(x), values(y)))
+        for z in (x, y):
+            for o in (z[1], z[2], z[4]):
+                o.close()
+
+
 def test_offsets_past_32_bits():
     """One tensor of more than 2^32 elements: its far end is read and written like its start."""
     n = (1 << 32) + 4099
