@@ -52,10 +52,6 @@ constexpr unsigned lds_for(int groups) { return groups >= 8 ? 0u : kCuLds / (gro
 
 // --------------------------------------------------------------- typed elements
 
-template <int DT> struct Elem { using T = float; };
-template <> struct Elem<FP8ADAM_BF16> { using T = uint16_t; };
-template <> struct Elem<FP8ADAM_F16> { using T = uint16_t; };
-
 constexpr int64_t dtype_bytes(int dt) { return dt == FP8ADAM_F32 ? 4 : 2; }
 
 typedef float vf2 __attribute__((ext_vector_type(2)));
@@ -64,10 +60,13 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 template <int DT>
 __device__ __forceinline__ float ld_elem(const void* base, int64_t i) {
-  if constexpr (DT == FP8ADAM_F32) return ld_global<float>(static_cast<const float*>(base) + i);
-  const uint16_t x = ld_global<uint16_t>(static_cast<const uint16_t*>(base) + i);
-  if constexpr (DT == FP8ADAM_BF16) return __uint_as_float((uint32_t)x << 16);
-  return (float)__builtin_bit_cast(_Float16, x);
+  if constexpr (DT == FP8ADAM_F32) {
+    return ld_global<float>(static_cast<const float*>(base) + i);
+  } else {
+    const uint16_t x = ld_global<uint16_t>(static_cast<const uint16_t*>(base) + i);
+    if constexpr (DT == FP8ADAM_BF16) return __uint_as_float((uint32_t)x << 16);
+    else return (float)__builtin_bit_cast(_Float16, x);
+  }
 }
 
 // To fp16 from a value that has been rounded to fp32: without the empty asm
@@ -168,13 +167,19 @@ struct AdamwDesc {
 };
 
 // One parameter group's constants, computed on the host from its hyperparameters.
+// The hardware's square root takes a subnormal v' as 0: next to an eps of 2^-38 or
+// more that is less than half an ulp of their sum.  For a smaller eps the host
+// scales the denominator by denom_scale = 2^12 (eps and step_size by as much,
+// inv_bc2 by its square, which lifts every subnormal): the same bits otherwise, at
+// no cost here.
 struct GroupConsts {
   float b1, omb1, b2, omb2;
   float lr_wd;      // lr * weight_decay
-  float step_size;  // lr / (1 - beta1^t)
-  float inv_bc2;    // 1 / (1 - beta2^t)
-  float eps;
+  float step_size;  // lr / (1 - beta1^t), times denom_scale
+  float inv_bc2;    // 1 / (1 - beta2^t), times its square
+  float eps;        // times denom_scale
 };
+inline double denom_scale(double eps) { return eps < 0x1p-38 ? 0x1p12 : 1.0; }
 struct AdamwConsts {
   GroupConsts g[FP8ADAM_MAX_GROUPS];
 };

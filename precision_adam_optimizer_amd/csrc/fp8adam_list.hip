@@ -140,6 +140,7 @@ __device__ __forceinline__ double total_of(const double* __restrict__ partial, i
 // does not need the sum is done before it.
 struct GroupRates {
   double lr[FP8ADAM_MAX_GROUPS], beta1[FP8ADAM_MAX_GROUPS], beta2[FP8ADAM_MAX_GROUPS];
+  double v_scale[FP8ADAM_MAX_GROUPS];  // denom_scale squared (lr carries denom_scale)
 };
 
 __global__ __launch_bounds__(kThreads) void k_list_ctl(const double* __restrict__ partial, int npartial,
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(kThreads) void k_list_ctl(const double* __restrict_
   if (q < n_groups) {
     const double t = (double)(was.step + 1);
     ctl->step_size[q] = (float)(R.lr[q] / (1.0 - pow(R.beta1[q], t)));
-    ctl->inv_bc2[q] = (float)(1.0 / (1.0 - pow(R.beta2[q], t)));
+    ctl->inv_bc2[q] = (float)(R.v_scale[q] / (1.0 - pow(R.beta2[q], t)));
   }
   const double sumsq = total_of(partial, npartial);
   if (threadIdx.x != 0) return;
@@ -655,8 +656,9 @@ int check_groups(const fp8adam_plan* p, const fp8adam_adamw_hparams* h, int32_t 
     if (!isfinite(h[q].lr) || !isfinite(h[q].weight_decay))
       return fail(FP8ADAM_EINVAL, "lr and weight_decay must be finite");
     // what the kernels take of them in fp32 (1 / (1 - beta) bounds the bias corrections)
-    if (!isfinite((float)(h[q].lr / (1.0 - h[q].beta1))) || !isfinite((float)(h[q].lr * h[q].weight_decay)) ||
-        !isfinite((float)h[q].eps) || !isfinite((float)(1.0 / (1.0 - h[q].beta2))))
+    const double sc = denom_scale(h[q].eps);
+    if (!isfinite((float)(h[q].lr * sc / (1.0 - h[q].beta1))) || !isfinite((float)(h[q].lr * h[q].weight_decay)) ||
+        !isfinite((float)h[q].eps) || !isfinite((float)(sc * sc / (1.0 - h[q].beta2))))
       return fail(FP8ADAM_EINVAL, "lr, lr * weight_decay, lr / (1 - beta1), 1 / (1 - beta2) and eps must be finite in fp32");
   }
   return 0;
@@ -671,9 +673,10 @@ void group_consts(const fp8adam_adamw_hparams* h, int n_groups, int64_t t, Adamw
     c.b2 = (float)h[q].beta2;
     c.omb2 = (float)(1.0 - h[q].beta2);
     c.lr_wd = (float)(h[q].lr * h[q].weight_decay);
-    c.eps = (float)h[q].eps;
-    c.step_size = t < 1 ? 0.0f : (float)(h[q].lr / (1.0 - pow(h[q].beta1, (double)t)));
-    c.inv_bc2 = t < 1 ? 0.0f : (float)(1.0 / (1.0 - pow(h[q].beta2, (double)t)));
+    const double sc = denom_scale(h[q].eps);
+    c.eps = (float)(h[q].eps * sc);
+    c.step_size = t < 1 ? 0.0f : (float)(h[q].lr * sc / (1.0 - pow(h[q].beta1, (double)t)));
+    c.inv_bc2 = t < 1 ? 0.0f : (float)(sc * sc / (1.0 - pow(h[q].beta2, (double)t)));
   }
 }
 
@@ -1049,7 +1052,9 @@ int fp8adam_adamw_step_amp(fp8adam_plan* plan, const fp8adam_adamw_hparams* grou
     group_consts(groups, n_groups, 0, C);
     GroupRates R{};
     for (int q = 0; q < n_groups; q++) {
-      R.lr[q] = groups[q].lr;
+      const double sc = denom_scale(groups[q].eps);
+      R.lr[q] = groups[q].lr * sc;
+      R.v_scale[q] = sc * sc;
       R.beta1[q] = groups[q].beta1;
       R.beta2[q] = groups[q].beta2;
     }

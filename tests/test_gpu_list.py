@@ -341,6 +341,28 @@ def test_adamw_nonfinite_and_zeros():
         opt.close()
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-25, 1e-20, 2.0 ** -38, 1e-8])
+@pytest.mark.parametrize("amp", [False, True])
+def test_adamw_tiny_gradients_and_eps(eps, amp):
+    """Gradients whose squares are subnormal in fp32, down to none, beside large ones: the weight is
+    the formula's for the moments that were stored (12u of the update, and the sum)."""
+    gr = torch.tensor([10.0 ** -k for k in range(-13, 23)], device="cuda")
+    p = torch.ones(gr.numel(), device="cuda")
+    opt = pk.AdamW([p], [gr])
+    hp = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=eps, weight_decay=0.0)
+    if amp:
+        opt.step_amp(pk.amp_state(1.0), **hp)
+    else:
+        opt.step(step=1, **hp)
+    m, v = opt.m[0].double().cpu(), opt.v[0].double().cpu()
+    assert float(v.min()) >= 0 and bool(((v > 0) & (v < 2.0 ** -126)).any())
+    upd = 1e-3 / (1 - 0.9) * m / ((v / (1 - 0.95)).sqrt() + eps)
+    some = (v > 0) | (eps > 0)
+    err = (p.double().cpu() - (1 - upd)).abs()
+    assert bool((err <= U * (13 * upd.abs() + 1.01) + 2.0 ** -148)[some].all()), (eps, err / U)
+    opt.close()
+
+
 def amp_fields(t):
     return pk.read_amp_state(t)
 
@@ -737,6 +759,45 @@ def test_amp_over_every_kind_in_one_list():
         for c in cases:
             c.check()
     opt.close()
+
+
+def moved(t, offset):
+    """t's values at that offset (in elements) into new memory."""
+    out = torch.zeros(t.numel() + offset, dtype=t.dtype, device="cuda")[offset:]
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("pd, cd, gd", [(F32, BF16, F16), (BF16, None, F16), (F16, None, F32)])
+@pytest.mark.parametrize("offs", [(1, 0, 0, 0, 0), (0, 1, 0, 0, 0), (0, 0, 1, 0, 0), (1, 1, 1, 2, 3), (1, 1, 1, 4, 4), (2, 2, 2, 3, 1)])
+def test_alignment_does_not_change_the_bits(bits, pd, cd, gd, offs):
+    """Weights, gradients, copies and moments each at their own offset: the aligned run's bits."""
+    for n in (1, 2, 130, 2049, 9000):
+        g = gen(n)
+        a = Case(n, g, pd, gd, cd, bits)
+        p, gr, m, v = (moved(x, o) for x, o in zip((a.p, a.g, a.m, a.v), (offs[0], offs[1], offs[3], offs[4])))
+        copy = moved(a.copy, offs[2]) if cd else None
+        state = ([m], [v]) if bits == 32 else ([m], [v], [moved(a.ms, 1)], [moved(a.vs, 1)])
+        x = optimizer([a])
+        y = pk.AdamW([p], [gr], copies=[copy], state_bits=bits, state=state)
+        for t in (1, 2):
+            x.step(step=t, **HP)
+            y.step(step=t, **HP)
+        assert torch.equal(a.p, p) and torch.equal(a.m, m) and torch.equal(a.v, v) and (not cd or torch.equal(a.copy, copy))
+        x.close()
+        y.close()
+        for granularity in ("block128", "tensor"):
+            q = [pk.Quantizer([z], granularity=granularity, codes=[moved(torch.zeros(n, dtype=torch.uint8, device="cuda"), o)])
+                 for z, o in ((a.g, 0), (gr, offs[3]))]
+            for k in q:
+                k.quantize()
+            assert torch.equal(q[0].codes[0], q[1].codes[0]) and torch.equal(q[0].scales[0], q[1].scales[0])
+            for k in q:
+                k.dequantize()
+            assert torch.equal(a.g, gr)
+            for k in q:
+                k.close()
 
 
 def test_two_plans_at_once():
