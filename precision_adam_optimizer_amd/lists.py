@@ -69,9 +69,9 @@ def _lib() -> ctypes.CDLL:
         L.fp8adam_plan_destroy.argtypes = [vp]
         L.fp8adam_plan_destroy.restype = None
         L.fp8adam_adamw_plan.argtypes = [P(vp), P(AdamwTensorArg), i32, P(AdamwConfigArg), vp]
-        # the hyperparameters by address, which the classes below keep: a call's pointer costs a small step 0.5 us
+        # the host structs by address, which the classes below keep: a pointer made for each call costs a small step 0.5 us
         L.fp8adam_adamw_step.argtypes = [vp, vp, i32, i64, vp]
-        L.fp8adam_adamw_step_amp.argtypes = [vp, vp, i32, P(AmpConfigArg), vp, vp]
+        L.fp8adam_adamw_step_amp.argtypes = [vp, vp, i32, vp, vp, vp]
         L.fp8adam_clip_plan.argtypes = [P(vp), P(ClipTensorArg), i32, vp]
         L.fp8adam_clip_grads.argtypes = [vp, ctypes.c_float, vp, vp]
         L.fp8adam_quant_plan.argtypes = [P(vp), P(QuantTensorArg), i32, P(QuantConfigArg), vp]
@@ -307,6 +307,8 @@ class AdamW(_Planned):
         self._hp = (AdamwHParamsArg * self.n_groups)()
         self._hp_at = ctypes.addressof(self._hp)
         self._given = None
+        self._amp = AmpConfigArg()
+        self._amp_at = ctypes.addressof(self._amp)
         self._build(dev, lambda: fp8adam_adamw_plan(args, cfg))
 
     def _set(self, lr, beta1, beta2, eps, weight_decay) -> None:
@@ -345,8 +347,10 @@ class AdamW(_Planned):
         if amp_state.device != self.device or not amp_state.is_contiguous():
             raise ValueError("amp_state must be contiguous and on the weights' device")
         self._set(lr, beta1, beta2, eps, weight_decay)
-        amp = AmpConfigArg(max_norm, growth_factor, backoff_factor, growth_interval)
-        self._call(_lib().fp8adam_adamw_step_amp, self._hp_at, self.n_groups, ctypes.byref(amp), amp_state.data_ptr())
+        a = self._amp
+        a.max_norm, a.growth_factor, a.backoff_factor, a.growth_interval = (max_norm, growth_factor, backoff_factor,
+                                                                            growth_interval)
+        self._call(_lib().fp8adam_adamw_step_amp, self._hp_at, self.n_groups, self._amp_at, amp_state.data_ptr())
 
     def checkpoint(self) -> list:
         """Copies of the moments in the form ``state=`` takes: [m, v, m_scale, v_scale].
