@@ -132,19 +132,48 @@ __device__ __forceinline__ void store4(Rsrc r, uint32_t o, const float (&x)[4]) 
   else __builtin_amdgcn_raw_buffer_store_b64(vu2{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])}, r, 2 * o, 0, POL);
 }
 
-// The codes of four values, to nearest even, saturating, where a NaN stays one
-// (the clamp of encode4 alone would make it -FMAX).  `odd`: the values' block or
-// tensor holds a NaN or Inf, which its amax tells; without one the test is not
-// made.
+// The codes of four values at the inverse scale of their own amax, to nearest even,
+// saturating, where a NaN stays one (the clamp of encode4 alone would make it
+// -FMAX).  `odd`: the amax is not finite; without that the test is not made.
 template <int FMT>
-__device__ __forceinline__ uint32_t encode4_nan(const float (&x)[4], bool odd) {
-  uint32_t w = encode4<FMT>(x[0], x[1], x[2], x[3]);
+__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, bool odd) {
+  const float q[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
+  uint32_t w = encode4<FMT>(q[0], q[1], q[2], q[3]);
   if (odd) {
 #pragma unroll
     for (int j = 0; j < 4; j++)
-      if (x[j] != x[j]) w |= 0x7Fu << (8 * j);  // a NaN code in both formats
+      if (q[j] != q[j]) w |= 0x7Fu << (8 * j);  // a NaN code in both formats
   }
   return w;
+}
+
+// codes4 where the scale s is a power of two and the POW2 scale of the amax, so that
+// no value passes FMAX: the scaled converts divide by it as they round (the same
+// codes as encode4 of x / s over 8.6e9 pairs of values and scales, every scale
+// exponent and results down to zero among them), without clamps and products.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4_pow2(const float (&x)[4], float s, bool odd) {
+  if (odd) return codes4<FMT>(x, 1.0f, true);  // such a block's scale is 1
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  s16x2 w{0, 0};
+  if constexpr (FMT == 0) {
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[0], x[1], s, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[2], x[3], s, true);
+  } else {
+    w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, x[0], x[1], s, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, x[2], x[3], s, true);
+  }
+  return __builtin_bit_cast(uint32_t, w);
+}
+
+// The largest of the 32 lanes of a half-wave, in each of them: four maxima with
+// fused DPP operands (every lane has a source), and lane ^ 16.
+__device__ __forceinline__ uint32_t half_wave_max(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));   // quad_perm [1,0,3,2]
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));   // quad_perm [2,3,0,1]
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));  // row_half_mirror
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, true));  // row_mirror
+  return max(x, (uint32_t)__builtin_amdgcn_ds_swizzle((int)x, 0x401F));
 }
 
 __device__ __forceinline__ bool nonfinite_amax(uint32_t amax_bits) { return amax_bits >= 0x7F800000u; }
@@ -222,21 +251,19 @@ constexpr int adamw_part_log2(int pd, bool s8) { return s8 && pd != FP8ADAM_F32 
 template <int MF, int VF>
 __device__ __forceinline__ void moments_to_codes(const float (&m1)[4], const float (&v1)[4], float& sm, float& sv,
                                                  uint32_t& wm, uint32_t& wv) {
-  float ism, isv;
   uint32_t am = 0, av = 0;
 #pragma unroll
   for (int j = 0; j < 4; j++) {
     am = max(am, abs_bits(m1[j]));
     av = max(av, abs_bits(v1[j]));
   }
-  am = group32_max(am);
-  av = group32_max(av);
-  choose_scale<MF, 0>(am, sm, ism);
-  choose_scale<VF, 0>(av, sv, isv);
-  const float qm[4] = {m1[0] * ism, m1[1] * ism, m1[2] * ism, m1[3] * ism};
-  const float qv[4] = {v1[0] * isv, v1[1] * isv, v1[2] * isv, v1[3] * isv};
-  wm = encode4_nan<MF>(qm, nonfinite_amax(am));
-  wv = encode4_nan<VF>(qv, nonfinite_amax(av));
+  am = half_wave_max(am);
+  av = half_wave_max(av);
+  float inv;
+  choose_scale<MF, 0>(am, sm, inv);
+  choose_scale<VF, 0>(av, sv, inv);
+  wm = codes4_pow2<MF>(m1, sm, nonfinite_amax(am));
+  wv = codes4_pow2<VF>(v1, sv, nonfinite_amax(av));
 }
 
 // One work-group per part.  32 lanes own one run of 128 elements (a block of

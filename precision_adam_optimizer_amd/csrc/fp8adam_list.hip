@@ -332,16 +332,14 @@ __device__ __forceinline__ void choose_scale_mode(uint32_t amax, int smode, floa
 
 // The new scale and the codes of a run of 128 values that 32 lanes hold, four each.
 template <int FMT>
-__device__ __forceinline__ uint32_t block_to_codes(float (&x)[4], int smode, float& s) {
+__device__ __forceinline__ uint32_t block_to_codes(const float (&x)[4], int smode, float& s) {
   uint32_t am = 0;
 #pragma unroll
   for (int j = 0; j < 4; j++) am = max(am, abs_bits(x[j]));
-  am = group32_max(am);
+  am = half_wave_max(am);
   float inv;
   choose_scale_mode<FMT>(am, smode, s, inv);
-#pragma unroll
-  for (int j = 0; j < 4; j++) x[j] *= inv;
-  return encode4_nan<FMT>(x, nonfinite_amax(am));
+  return codes4<FMT>(x, inv, nonfinite_amax(am));
 }
 
 // One work-group per part, 32 lanes per block of 128, four consecutive elements
@@ -465,9 +463,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_tensor(const QuantDesc* __re
     for (int u = 0; u < kU; u++) {
       float x[4];
       unpack4<DT>(r[u], x);
-#pragma unroll
-      for (int j = 0; j < 4; j++) x[j] *= inv;
-      __builtin_amdgcn_raw_buffer_store_b32(encode4_nan<FMT>(x, odd), bc, 4 * threadIdx.x + u * kSubTile, 0, kStPol);
+      __builtin_amdgcn_raw_buffer_store_b32(codes4<FMT>(x, inv, odd), bc, 4 * threadIdx.x + u * kSubTile, 0, kStPol);
     }
   }
   const bool first = w == d.part0;
@@ -475,8 +471,8 @@ __global__ __launch_bounds__(kThreads) void k_quant_tensor(const QuantDesc* __re
   // what is not in groups: all of another part, and the elements in front of the first
   const int64_t from = first ? 0 : lo, to = whole ? first ? (int64_t)d.head : lo : min(lo + kLen, d.numel);
   for (int64_t i = from + threadIdx.x; i < to; i += kThreads) {
-    const float x[4] = {ld_elem<DT>(d.x, i) * inv, 0.0f, 0.0f, 0.0f};
-    st_global<uint8_t>(d.codes + i, (uint8_t)encode4_nan<FMT>(x, odd));
+    const float x[4] = {ld_elem<DT>(d.x, i), 0.0f, 0.0f, 0.0f};
+    st_global<uint8_t>(d.codes + i, (uint8_t)codes4<FMT>(x, inv, odd));
   }
 }
 
