@@ -166,11 +166,39 @@ __global__ __launch_bounds__(kReduceThreads) void k_gradctl(const double* __rest
     __syncthreads();
   }
   if (threadIdx.x != 0) return;
-  float gfac;
-  int64_t t;
-  if (!scaler_decide(st, load_scaler(st), cfg, sacc[0], sbad[0] > 0.0, gfac, t)) {
+  const float scale = st->scale;
+  const float inv = __double2float_rn(__ddiv_rn(1.0, (double)scale));
+  if (sbad[0] > 0.0) {
+    st_global(&st->found_inf, 1);
+    st_global(&st->grad_norm, __builtin_nanf(""));
+    st_global(&st->clip_coef, 1.0f);
+    st_global(&st->grad_factor, 0.0f);
+    st_global(&st->scale, __fmul_rn(scale, cfg.backoff_factor));
+    st_global(&st->growth_tracker, 0);
     st_global(&ctl->skip, 1);
     return;
+  }
+  const double norm = __dmul_rn(__dsqrt_rn(sacc[0]), (double)inv);
+  double cc = 1.0;
+  if (cfg.max_norm > 0.0f) {
+    cc = __ddiv_rn((double)cfg.max_norm, __dadd_rn(norm, 1e-6));
+    if (cc > 1.0) cc = 1.0;
+  }
+  const float c32 = __double2float_rn(cc);
+  const float gfac = __fmul_rn(c32, inv);
+  const int64_t t = st->step + 1;
+  st_global(&st->found_inf, 0);
+  st_global(&st->grad_norm, __double2float_rn(norm));
+  st_global(&st->clip_coef, c32);
+  st_global(&st->grad_factor, gfac);
+  st_global(&st->step, t);
+  const int32_t next = st->growth_tracker + 1;
+  if (next == cfg.growth_interval) {
+    const float grown = __fmul_rn(scale, cfg.growth_factor);
+    if (isfinite(grown)) st_global(&st->scale, grown);
+    st_global(&st->growth_tracker, 0);
+  } else {
+    st_global(&st->growth_tracker, next);
   }
   const double bc1 = 1.0 - pow((double)beta1, (double)t), bc2 = 1.0 - pow((double)beta2, (double)t);
   st_global(&ctl->skip, 0);

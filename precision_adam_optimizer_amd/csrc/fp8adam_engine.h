@@ -553,60 +553,6 @@ __device__ __forceinline__ void delayed_scale(const float* h, const StepConsts& 
   choose_scale<FMT, SMODE>(abs_bits(__uint_as_float(r) * c.margin_scale), s, inv);
 }
 
-// What the loss scaler's decision reads of its state: loaded before the sum that
-// the decision waits for.
-struct ScalerState {
-  float scale;
-  int32_t growth_tracker;
-  int64_t step;
-};
-
-__device__ __forceinline__ ScalerState load_scaler(const fp8adam_amp_state* st) {
-  return ScalerState{ld_global<float>(&st->scale), ld_global<int32_t>(&st->growth_tracker), ld_global<int64_t>(&st->step)};
-}
-
-// The loss scaler's decision (one thread): from the sum of squares of every
-// (scaled) gradient and whether one was not finite, update the state `st` (which
-// held `was`) and return true with the gradient factor and the step's t, or false
-// if the step is skipped.
-__device__ inline bool scaler_decide(fp8adam_amp_state* st, const ScalerState& was, const fp8adam_amp_config& cfg,
-                                     double sumsq, bool bad, float& gfac, int64_t& t) {
-  const float scale = was.scale;
-  const float inv = __double2float_rn(__ddiv_rn(1.0, (double)scale));
-  if (bad) {
-    st_global(&st->found_inf, 1);
-    st_global(&st->grad_norm, __builtin_nanf(""));
-    st_global(&st->clip_coef, 1.0f);
-    st_global(&st->grad_factor, 0.0f);
-    st_global(&st->scale, __fmul_rn(scale, cfg.backoff_factor));
-    st_global(&st->growth_tracker, 0);
-    return false;
-  }
-  const double norm = __dmul_rn(__dsqrt_rn(sumsq), (double)inv);
-  double cc = 1.0;
-  if (cfg.max_norm > 0.0f) {
-    cc = __ddiv_rn((double)cfg.max_norm, __dadd_rn(norm, 1e-6));
-    if (cc > 1.0) cc = 1.0;
-  }
-  const float c32 = __double2float_rn(cc);
-  gfac = __fmul_rn(c32, inv);
-  t = was.step + 1;
-  st_global(&st->found_inf, 0);
-  st_global(&st->grad_norm, __double2float_rn(norm));
-  st_global(&st->clip_coef, c32);
-  st_global(&st->grad_factor, gfac);
-  st_global(&st->step, t);
-  const int32_t next = was.growth_tracker + 1;
-  if (next == cfg.growth_interval) {
-    const float grown = __fmul_rn(scale, cfg.growth_factor);
-    if (isfinite(grown)) st_global(&st->scale, grown);
-    st_global(&st->growth_tracker, 0);
-  } else {
-    st_global(&st->growth_tracker, next);
-  }
-  return true;
-}
-
 // ------------------------------------------------------------------ pass 1
 
 // The amax of |m'| and of v' over the elements [start, end) of tensor d (whole

@@ -741,6 +741,32 @@ def test_a_list_of_thousands_equals_one_tensor(pd, gd):
         o.close()
 
 
+def test_amp_state_goes_as_in_the_fp8_step():
+    """The scaler's state after each call is FP8AdamW.step_amp's on the same gradients: taken and
+    skipped calls, growth and backoff, clipped and not (the norm within its rounding: its partial
+    sums differ)."""
+    g = gen(18)
+    grads = [filled(n, BF16, g, 20.0) for n in (5000, 300)]
+    ps = [[torch.zeros(n, device="cuda") for n in (5000, 300)] for _ in range(2)]
+    a, b = pk.AdamW(ps[0], grads), pk.FP8AdamW(ps[1], grads)
+    sa, sb = pk.amp_state(64.0), pk.amp_state(64.0)
+    for call in range(1, 9):
+        for x in grads:
+            x.copy_(torch.randn(x.numel(), generator=g, device="cuda") * (0.01 if call % 3 == 0 else 20.0))
+        if call in (3, 6):
+            grads[1][7] = math.inf
+        kw = dict(max_norm=1.0, growth_interval=2, growth_factor=4.0, backoff_factor=0.25)
+        a.step_amp(sa, **HP, **kw)
+        b.step_amp(sb, step=call, **HP, **kw)
+        x, y = amp_fields(sa), amp_fields(sb)
+        for k in ("scale", "growth_tracker", "step", "found_inf"):
+            assert x[k] == y[k], (call, k)
+        for k in ("grad_norm", "clip_coef", "grad_factor"):
+            assert x[k] == y[k] or abs(x[k] - y[k]) <= 2 * U * abs(y[k]) or (math.isnan(x[k]) and math.isnan(y[k])), (call, k)
+    a.close()
+    b.close()
+
+
 def test_amp_over_every_kind_in_one_list():
     """One norm over gradients of three types, then every kind of tensor with the same factor."""
     g = gen(15)
