@@ -25,8 +25,8 @@ using namespace fp8adam_engine;
 // order each XCD takes runs of kXcdRun consecutive parts, and the XCDs take
 // neighbouring runs, so that the whole chip works on one stretch of the list.
 // Measured with 32-part runs (of 1024 elements) against parts round-robin and
-// against one contiguous eighth of the list per XCD: 842M weights with 32-bit
-// moments 4.08, 4.24 and 4.17 ms; 842M bf16 weights with 8-bit moments 1.36, 1.42
+// against one contiguous eighth of the list per XCD, with eight work-groups on a CU:
+// 842M weights with 32-bit moments 4.08, 4.24 and 4.17 ms; 842M bf16 weights with 8-bit moments 1.36, 1.42
 // and 1.40 ms; 7M weights in ragged tensors 36, 37 and 40 us.  Runs of 16 and of
 // 64 are 2 to 6% slower on the largest.  A surplus work-group gets -1.
 constexpr int64_t kXcdRun = 32;
@@ -240,8 +240,8 @@ __device__ __forceinline__ float adamw_element(const GroupConsts& c, float g, fl
 }
 
 // log2 of a part's elements: 256 lanes of 4, twice where an element moves few bytes
-// (8-bit moments of 16-bit weights).  842M fp32 weights with 32-bit moments: 1024
-// elements 4.15 ms, 2048 4.24, 4096 4.35; 109.5M with 8-bit moments, scaled and
+// (8-bit moments of 16-bit weights).  With eight work-groups on a CU, 842M fp32
+// weights with 32-bit moments: 1024 elements 4.15 ms, 2048 4.24, 4096 4.35; 109.5M with 8-bit moments, scaled and
 // clipped: 1024 320 us, 2048 330; 842M bf16 weights with 8-bit moments: 1024 1.37
 // ms, 2048 1.36, 4096 1.44.
 constexpr int adamw_part_log2(int pd, bool s8) { return s8 && pd != FP8ADAM_F32 ? 11 : 10; }

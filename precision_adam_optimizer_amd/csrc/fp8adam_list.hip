@@ -48,8 +48,9 @@ struct GradDesc {
 
 // Two work-groups per CU with 8 16-byte loads per lane keep the norm pass at the
 // read-only rate (7.0 TB/s), and the clipping pass, whose every work-group sums
-// the partials, reads few of them: clipping 842M fp32 gradients to bf16 takes 1264
-// us with 512, 1284 with 2048.
+// the partials, reads few of them: clipping 842M fp32 gradients to bf16 took 1264
+// us with 512 and 1284 with 2048 (both passes, parts in plain order; 1229 us with
+// the order of k_list_clip).
 constexpr int kListNormGroups = 512;
 
 __device__ __forceinline__ void sumsq_word(uint32_t x, double& acc, std::integral_constant<int, FP8ADAM_F32>) {
@@ -316,11 +317,12 @@ __device__ __forceinline__ void scale_range_to(const GradDesc& d, int64_t lo, in
 // order everywhere) and scales its 2^kClipPartLog2 elements, from the list's end to
 // its start: what the norm pass read last may still be in the last-level cache (1%
 // of 109.5M fp32).  842M fp32 gradients into bf16 take 770 us (6.6 TB/s); a fixed
-// grid striding over the list took 918.  Letting the norm pass's
-// last work-group finish the sum instead costs each of them a release to the other
-// XCDs: 137 us against 34 for 219 MB.
+// grid striding over the list took 918.  Letting the norm pass's last work-group
+// finish the sum instead costs each of them a release to the other XCDs: 137 us
+// against 34 for 219 MB in 2048 work-groups.
 constexpr int kClipPartLog2 = 12;
-constexpr int64_t kClipXcdRun = 16;  // parts in an XCD's run: 1233 us (both passes) against 1247 with 32, 1264 in plain order
+// Parts in an XCD's run: 842M take 1233 us (both passes), 1247 with 32, 1264 in plain order.
+constexpr int64_t kClipXcdRun = 16;
 constexpr int kGradChunkMinLog2 = 12, kGradChunkMaxLog2 = 15;
 static_assert(kClipPartLog2 <= kGradChunkMinLog2, "a chunk holds whole parts");
 
@@ -369,8 +371,8 @@ struct QuantDesc {
 };
 
 // log2 of the elements of a one-shot work-group.  Blocks, both ways: 2048 (109.5M
-// fp32 to E4M3 blocks 83 us, back 93 us; 1024: 93 and 99, 4096: 85 and 98, 8192: 91
-// and 103).  With a tensor's scale: 4096 (202M bf16 in 150 us; 2048: 161, 8192: 153),
+// fp32 to E4M3 blocks 83 us, back 93 us with eight work-groups on a CU; 1024: 93 and
+// 99, 4096: 85 and 98, 8192: 91 and 103; dequant_lds takes the 93 to 83).  With a tensor's scale: 4096 (202M bf16 in 150 us; 2048: 161, 8192: 153),
 // since each wave reads the tensor's maxima first.
 constexpr int kQuantPartLog2 = 11;
 constexpr int kQuantTensorPartLog2 = 12;
