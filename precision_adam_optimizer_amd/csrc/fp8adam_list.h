@@ -87,22 +87,56 @@ __device__ __forceinline__ void st_elem(void* base, int64_t i, float x) {
   else st_global<uint16_t>(static_cast<uint16_t*>(base) + i, __builtin_bit_cast(uint16_t, to_f16(x)));
 }
 
-// Four consecutive elements through a buffer resource, at element offset o of its
-// base (dword-aligned: 16 bytes of fp32 or 8 of a 16-bit type per lane).
+// Four consecutive elements of a type, or four codes, as they lie in memory.
+constexpr int kCodes = -1;
 template <int DT> struct Raw4 { vu2 x; };
 template <> struct Raw4<FP8ADAM_F32> { vu4 x; };
+template <> struct Raw4<kCodes> { uint32_t x; };
+
+constexpr int64_t elem_bytes(int dt) { return dt == kCodes ? 1 : dt == FP8ADAM_F32 ? 4 : 2; }
+
+// A whole part of one stream, accessed four elements per lane, non-temporally.
+// DWORD: it starts on a dword, and goes through a buffer resource, which streams
+// faster (the updates' byte mixes 6.4 against 6.0 TB/s).  Otherwise it starts on
+// any element, and goes through global instructions, which take any address.
+template <int DT, bool DWORD>
+struct Stream {
+  Rsrc r;
+  __device__ __forceinline__ Stream(const void* base, int64_t first, int64_t n)
+      : r(rsrc(static_cast<const char*>(base) + elem_bytes(DT) * first, elem_bytes(DT) * n)) {}
+  __device__ __forceinline__ Raw4<DT> load(uint32_t o) const {
+    if constexpr (DT == kCodes) return Raw4<DT>{__builtin_amdgcn_raw_buffer_load_b32(r, o, 0, kLdPol)};
+    else if constexpr (DT == FP8ADAM_F32) return Raw4<DT>{__builtin_amdgcn_raw_buffer_load_b128(r, 4 * o, 0, kLdPol)};
+    else return Raw4<DT>{__builtin_amdgcn_raw_buffer_load_b64(r, 2 * o, 0, kLdPol)};
+  }
+  __device__ __forceinline__ void store(uint32_t o, const Raw4<DT>& w) const {
+    if constexpr (DT == kCodes) __builtin_amdgcn_raw_buffer_store_b32(w.x, r, o, 0, kStPol);
+    else if constexpr (DT == FP8ADAM_F32) __builtin_amdgcn_raw_buffer_store_b128(w.x, r, 4 * o, 0, kStPol);
+    else __builtin_amdgcn_raw_buffer_store_b64(w.x, r, 2 * o, 0, kStPol);
+  }
+};
+
+typedef vu4 __attribute__((aligned(4))) vu4_any;
+typedef vu2 __attribute__((aligned(2))) vu2_any;
+typedef uint32_t __attribute__((aligned(1))) u32_any;
 
 template <int DT>
-__device__ __forceinline__ Rsrc typed_rsrc(const void* base, int64_t first, int64_t n) {
-  constexpr int64_t B = DT == FP8ADAM_F32 ? 4 : 2;
-  return rsrc(static_cast<const char*>(base) + B * first, B * n);
-}
-
-template <int DT, int POL = kLdPol>
-__device__ __forceinline__ Raw4<DT> load4(Rsrc r, uint32_t o) {
-  if constexpr (DT == FP8ADAM_F32) return Raw4<DT>{__builtin_amdgcn_raw_buffer_load_b128(r, 4 * o, 0, POL)};
-  else return Raw4<DT>{__builtin_amdgcn_raw_buffer_load_b64(r, 2 * o, 0, POL)};
-}
+struct Stream<DT, false> {
+  const char* p;
+  __device__ __forceinline__ Stream(const void* base, int64_t first, int64_t)
+      : p(static_cast<const char*>(base) + elem_bytes(DT) * first) {}
+  __device__ __forceinline__ Raw4<DT> load(uint32_t o) const {
+    if constexpr (DT == kCodes) return Raw4<DT>{ld_stream<u32_any, true>(p + o)};
+    else if constexpr (DT == FP8ADAM_F32) return Raw4<DT>{ld_stream<vu4_any, true>(p + 4 * o)};
+    else return Raw4<DT>{ld_stream<vu2_any, true>(p + 2 * o)};
+  }
+  __device__ __forceinline__ void store(uint32_t o, const Raw4<DT>& w) const {
+    char* q = const_cast<char*>(p);
+    if constexpr (DT == kCodes) st_stream<u32_any, true>(q + o, w.x);
+    else if constexpr (DT == FP8ADAM_F32) st_stream<vu4_any, true>(q + 4 * o, w.x);
+    else st_stream<vu2_any, true>(q + 2 * o, w.x);
+  }
+};
 
 template <int DT>
 __device__ __forceinline__ void unpack4(const Raw4<DT>& w, float (&x)[4]) {
@@ -124,12 +158,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   else return __builtin_bit_cast(uint32_t, f16x2{to_f16(a), to_f16(b)});
 }
 
-template <int DT, int POL = kStPol>
-__device__ __forceinline__ void store4(Rsrc r, uint32_t o, const float (&x)[4]) {
+template <int DT>
+__device__ __forceinline__ Raw4<DT> pack4(const float (&x)[4]) {
   if constexpr (DT == FP8ADAM_F32)
-    __builtin_amdgcn_raw_buffer_store_b128(
-        vu4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])}, r, 4 * o, 0, POL);
-  else __builtin_amdgcn_raw_buffer_store_b64(vu2{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])}, r, 2 * o, 0, POL);
+    return Raw4<DT>{vu4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])}};
+  else return Raw4<DT>{vu2{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])}};
 }
 
 // The codes of four values at the inverse scale of their own amax, to nearest even,
@@ -191,8 +224,9 @@ struct AdamwDesc {
   int64_t numel;
   int64_t part0;   // the tensor's first part in its kind's table
   int32_t group;
-  int16_t head;    // elements in front of the first part (0 or 1), which the first part's work-group does alone
-  int16_t vec;     // every stream starts on a dword at element `head`
+  int32_t head;    // elements in front of the first part (0 or 1), which the first part's work-group does alone
+  int32_t vec;     // every stream starts on a dword at element `head` (otherwise head is 0)
+  int32_t pad;
 };
 
 // One parameter group's constants, computed on the host from its hyperparameters.
@@ -266,11 +300,76 @@ __device__ __forceinline__ void moments_to_codes(const float (&m1)[4], const flo
   wv = codes4_pow2<VF>(v1, sv, nonfinite_amax(av));
 }
 
+// A whole part, [lo, lo + 2^PL), in groups of four consecutive elements per lane.
+template <bool DWORD, int PL, int PD, int CD, int GD, bool S8, int MF, int VF>
+__device__ __forceinline__ void adamw_whole(const AdamwDesc& d, const GroupConsts& c, float gfac, int64_t lo) {
+  constexpr int64_t kLen = (int64_t)1 << PL;
+  constexpr int kU = (int)(kLen / kSubTile);
+  constexpr int MD = S8 ? kCodes : FP8ADAM_F32;
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const Stream<PD, DWORD> sp(d.p, lo, kLen);
+  const Stream<GD, DWORD> sg(d.g, lo, kLen);
+  const Stream<MD, DWORD> smom(d.m, lo, kLen), svar(d.v, lo, kLen);
+  Raw4<PD> rp[kU];
+  Raw4<GD> rg[kU];
+  Raw4<MD> rm[kU], rv[kU];
+  float sm[kU], sv[kU];
+  const int64_t block0 = (lo >> 7) + run;
+#pragma unroll
+  for (int u = 0; u < kU; u++) {
+    const uint32_t o = 4 * threadIdx.x + u * kSubTile;
+    rg[u] = sg.load(o);
+    rm[u] = smom.load(o);
+    rv[u] = svar.load(o);
+    if constexpr (S8) {
+      sm[u] = ld_global<float>(d.sm + block0 + 8 * u);
+      sv[u] = ld_global<float>(d.sv + block0 + 8 * u);
+    }
+    rp[u] = sp.load(o);
+  }
+#pragma unroll
+  for (int u = 0; u < kU; u++) {
+    const uint32_t o = 4 * threadIdx.x + u * kSubTile;
+    float p[4], g[4], m[4], v[4], m1[4], v1[4];
+    unpack4<GD>(rg[u], g);
+    if constexpr (S8) {
+      decode4<MF>(rm[u].x, m);
+      decode4<VF>(rv[u].x, v);
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        m[j] *= sm[u];
+        v[j] *= sv[u];
+      }
+    } else {
+      unpack4<FP8ADAM_F32>(rm[u], m);
+      unpack4<FP8ADAM_F32>(rv[u], v);
+    }
+    unpack4<PD>(rp[u], p);
+#pragma unroll
+    for (int j = 0; j < 4; j++) p[j] = adamw_element(c, g[j] * gfac, p[j], m[j], v[j], m1[j], v1[j]);
+    sp.store(o, pack4<PD>(p));
+    if constexpr (CD != 0) Stream<CD, DWORD>(d.copy, lo, kLen).store(o, pack4<CD>(p));
+    if constexpr (S8) {
+      uint32_t wm, wv;
+      float ns, nv;
+      moments_to_codes<MF, VF>(m1, v1, ns, nv, wm, wv);
+      smom.store(o, Raw4<MD>{wm});
+      svar.store(o, Raw4<MD>{wv});
+      if (lane == 0) {
+        st_global<float>(d.sm + block0 + 8 * u, ns);
+        st_global<float>(d.sv + block0 + 8 * u, nv);
+      }
+    } else {
+      smom.store(o, pack4<FP8ADAM_F32>(m1));
+      svar.store(o, pack4<FP8ADAM_F32>(v1));
+    }
+  }
+}
+
 // One work-group per part.  32 lanes own one run of 128 elements (a block of
-// 8-bit moments).  A whole part of a tensor whose streams start on dwords goes in
-// groups of four consecutive elements per lane, through buffer resources; another
-// one element by element, where lane h of the 32 holds elements h, h + 32, h + 64
-// and h + 96 of its run, so that accesses are contiguous at any alignment.
+// 8-bit moments).  A whole part goes in groups of four consecutive elements per
+// lane, the last part of a tensor element by element, where lane h of the 32 holds
+// elements h, h + 32, h + 64 and h + 96 of its run.
 //
 // Bound by HBM, each stream read and written once (counters: 14.0 bytes fetched and
 // 14.0 written per fp32 weight with a bf16 gradient, a bf16 copy and 32-bit
@@ -303,67 +402,9 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamwDesc* __restrict_
   const int64_t lo = d.head + ((w - d.part0) << PL);
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;  // of 8 runs per tile of 1024
   if (d.vec && lo + kLen <= d.numel) {
-    const Rsrc bp = typed_rsrc<PD>(d.p, lo, kLen), bg = typed_rsrc<GD>(d.g, lo, kLen);
-    const Rsrc bm = S8 ? rsrc(static_cast<uint8_t*>(d.m) + lo, kLen) : typed_rsrc<FP8ADAM_F32>(d.m, lo, kLen);
-    const Rsrc bv = S8 ? rsrc(static_cast<uint8_t*>(d.v) + lo, kLen) : typed_rsrc<FP8ADAM_F32>(d.v, lo, kLen);
-    Raw4<PD> rp[kU];
-    Raw4<GD> rg[kU];
-    Raw4<FP8ADAM_F32> rm[kU], rv[kU];
-    uint32_t cm[kU], cv[kU];
-    float sm[kU], sv[kU];
-    const int64_t block0 = (lo >> 7) + run;
-#pragma unroll
-    for (int u = 0; u < kU; u++) {
-      const uint32_t o = 4 * threadIdx.x + u * kSubTile;
-      rg[u] = load4<GD>(bg, o);
-      if constexpr (S8) {
-        cm[u] = __builtin_amdgcn_raw_buffer_load_b32(bm, o, 0, kLdPol);
-        cv[u] = __builtin_amdgcn_raw_buffer_load_b32(bv, o, 0, kLdPol);
-        sm[u] = ld_global<float>(d.sm + block0 + 8 * u);
-        sv[u] = ld_global<float>(d.sv + block0 + 8 * u);
-      } else {
-        rm[u] = load4<FP8ADAM_F32>(bm, o);
-        rv[u] = load4<FP8ADAM_F32>(bv, o);
-      }
-      rp[u] = load4<PD>(bp, o);
-    }
-#pragma unroll
-    for (int u = 0; u < kU; u++) {
-      const uint32_t o = 4 * threadIdx.x + u * kSubTile;
-      float p[4], g[4], m[4], v[4], m1[4], v1[4];
-      unpack4<GD>(rg[u], g);
-      if constexpr (S8) {
-        decode4<MF>(cm[u], m);
-        decode4<VF>(cv[u], v);
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          m[j] *= sm[u];
-          v[j] *= sv[u];
-        }
-      } else {
-        unpack4<FP8ADAM_F32>(rm[u], m);
-        unpack4<FP8ADAM_F32>(rv[u], v);
-      }
-      unpack4<PD>(rp[u], p);
-#pragma unroll
-      for (int j = 0; j < 4; j++) p[j] = adamw_element(c, g[j] * gfac, p[j], m[j], v[j], m1[j], v1[j]);
-      store4<PD>(bp, o, p);
-      if constexpr (CD != 0) store4<CD>(typed_rsrc<CD>(d.copy, lo, kLen), o, p);
-      if constexpr (S8) {
-        uint32_t wm, wv;
-        float ns, nv;
-        moments_to_codes<MF, VF>(m1, v1, ns, nv, wm, wv);
-        __builtin_amdgcn_raw_buffer_store_b32(wm, bm, o, 0, kStPol);
-        __builtin_amdgcn_raw_buffer_store_b32(wv, bv, o, 0, kStPol);
-        if (lane == 0) {
-          st_global<float>(d.sm + block0 + 8 * u, ns);
-          st_global<float>(d.sv + block0 + 8 * u, nv);
-        }
-      } else {
-        store4<FP8ADAM_F32>(bm, o, m1);
-        store4<FP8ADAM_F32>(bv, o, v1);
-      }
-    }
+    adamw_whole<true, PL, PD, CD, GD, S8, MF, VF>(d, c, gfac, lo);
+  } else if (lo + kLen <= d.numel) {
+    adamw_whole<false, PL, PD, CD, GD, S8, MF, VF>(d, c, gfac, lo);
   } else {
     for (int u = 0; u < kU; u++) {
       const int64_t first = lo + u * kSubTile + run * kBlock, block = first >> 7;

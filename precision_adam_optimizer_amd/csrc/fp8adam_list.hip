@@ -271,37 +271,42 @@ static_assert(kTicketGroups <= 64, "one wave sums the partials");
 
 constexpr int kClipUnroll = 4;
 
-// dst = src * coef over [lo, hi).  Groups of four elements per lane wherever every
-// group starts on a dword in both, after one single element where the 16-bit
-// pointers are both off by one; element by element otherwise (two 16-bit types of
-// which one is off by one).
-template <int SD, int DD>
-__device__ __forceinline__ void scale_range(const GradDesc& d, int64_t lo, int64_t hi, float coef) {
-  constexpr int SB = SD == FP8ADAM_F32 ? 4 : 2, DB = DD == FP8ADAM_F32 ? 4 : 2;
-  const char* src = static_cast<const char*>(d.src) + SB * lo;
-  char* dst = static_cast<char*>(d.dst) + DB * lo;
-  const int n = (int)(hi - lo);
-  const int soff = SB == 2 ? (int)((uintptr_t)src >> 1 & 1u) : -1, doff = DB == 2 ? (int)((uintptr_t)dst >> 1 & 1u) : -1;
-  const int head = max(max(soff, doff), 0);
-  if (soff >= 0 && doff >= 0 && soff != doff) {  // uniform
-    for (int i = threadIdx.x; i < n; i += kThreads) st_elem<DD>(dst, i, ld_elem<SD>(src, i) * coef);
-    return;
-  }
-  const int nvec = max(n - head, 0) >> 2, tail = head + 4 * nvec;
-  const Rsrc rs = typed_rsrc<SD>(src, head, 4 * nvec), rd = typed_rsrc<DD>(dst, head, 4 * nvec);
-  for (int v = threadIdx.x; v < nvec; v += kThreads * kClipUnroll) {
+template <int SD, int DD, bool DWORD>
+__device__ __forceinline__ void scale_groups(const char* src, char* dst, int first, int ngroups, float coef) {
+  const Stream<SD, DWORD> ss(src, first, 4 * ngroups);
+  const Stream<DD, DWORD> sd(dst, first, 4 * ngroups);
+  for (int v = threadIdx.x; v < ngroups; v += kThreads * kClipUnroll) {
     Raw4<SD> w[kClipUnroll];
 #pragma unroll
-    for (int u = 0; u < kClipUnroll; u++) w[u] = load4<SD>(rs, 4 * (v + u * kThreads));
+    for (int u = 0; u < kClipUnroll; u++)
+      if (DWORD || v + u * kThreads < ngroups) w[u] = ss.load(4 * (v + u * kThreads));
 #pragma unroll
     for (int u = 0; u < kClipUnroll; u++) {
       float x[4];
       unpack4<SD>(w[u], x);
 #pragma unroll
       for (int j = 0; j < 4; j++) x[j] *= coef;
-      store4<DD>(rd, 4 * (v + u * kThreads), x);  // one behind the last vector is dropped
+      // (a buffer resource drops what lies behind the last group)
+      if (DWORD || v + u * kThreads < ngroups) sd.store(4 * (v + u * kThreads), pack4<DD>(x));
     }
   }
+}
+
+// dst = src * coef over [lo, hi), in groups of four elements per lane: on dwords in
+// both, after one single element where the 16-bit pointers are all off by one;
+// from any element where one of two 16-bit pointers is.
+template <int SD, int DD>
+__device__ __forceinline__ void scale_range(const GradDesc& d, int64_t lo, int64_t hi, float coef) {
+  const char* src = static_cast<const char*>(d.src) + elem_bytes(SD) * lo;
+  char* dst = static_cast<char*>(d.dst) + elem_bytes(DD) * lo;
+  const int n = (int)(hi - lo);
+  const int soff = SD != FP8ADAM_F32 ? (int)((uintptr_t)src >> 1 & 1u) : -1;
+  const int doff = DD != FP8ADAM_F32 ? (int)((uintptr_t)dst >> 1 & 1u) : -1;
+  const bool dword = soff < 0 || doff < 0 || soff == doff;  // uniform
+  const int head = dword ? max(max(soff, doff), 0) : 0;
+  const int ngroups = max(n - head, 0) >> 2, tail = head + 4 * ngroups;
+  if (dword) scale_groups<SD, DD, true>(src, dst, head, ngroups, coef);
+  else scale_groups<SD, DD, false>(src, dst, head, ngroups, coef);
   const int single = (int)threadIdx.x < head ? (int)threadIdx.x : tail + (int)threadIdx.x - head;
   if (single < n) st_elem<DD>(dst, single, ld_elem<SD>(src, single) * coef);
 }
@@ -398,10 +403,28 @@ __device__ __forceinline__ uint32_t block_to_codes(const float (&x)[4], int smod
   return codes4<FMT>(x, inv, nonfinite_amax(am));
 }
 
+template <bool DWORD, int DT, int FMT>
+__device__ __forceinline__ void quant_block_whole(const QuantDesc& d, int64_t lo, int smode) {
+  constexpr int64_t kLen = (int64_t)1 << kQuantPartLog2;
+  constexpr int kU = (int)(kLen / kSubTile);
+  const Stream<DT, DWORD> sx(d.x, lo, kLen);
+  const Stream<kCodes, DWORD> sc(d.codes, lo, kLen);
+  Raw4<DT> r[kU];
+#pragma unroll
+  for (int u = 0; u < kU; u++) r[u] = sx.load(4 * threadIdx.x + u * kSubTile);
+#pragma unroll
+  for (int u = 0; u < kU; u++) {
+    float x[4], s;
+    unpack4<DT>(r[u], x);
+    sc.store(4 * threadIdx.x + u * kSubTile, Raw4<kCodes>{block_to_codes<FMT>(x, smode, s)});
+    if ((threadIdx.x & 31) == 0) st_global<float>(d.scale + (lo >> 7) + 8 * u + (threadIdx.x >> 5), s);
+  }
+}
+
 // One work-group per part, 32 lanes per block of 128, four consecutive elements
-// per lane; in a part that is not whole or not dword-aligned lane h takes the
-// block's elements h, h + 32, h + 64, h + 96.  Bound by HBM: 109.5M fp32 (5.03 bytes
-// each) in 83 us, 6.6 TB/s, 97% of its reads and writes at their own rates.
+// per lane; in the last part of a tensor lane h takes the block's elements h,
+// h + 32, h + 64, h + 96.  Bound by HBM: 109.5M fp32 (5.03 bytes each) in 83 us, 6.6
+// TB/s, 97% of its reads and writes at their own rates.
 template <int DT, int FMT>
 __global__ __launch_bounds__(kThreads) void k_quant_block(const QuantDesc* __restrict__ descs,
                                                           const int32_t* __restrict__ part_tid, int64_t nparts,
@@ -413,19 +436,13 @@ __global__ __launch_bounds__(kThreads) void k_quant_block(const QuantDesc* __res
   const QuantDesc d = descs[part_tid[w]];
   const int64_t lo = (w - d.part0) << kQuantPartLog2;
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
-  if (d.vec && lo + kLen <= d.numel) {
-    const Rsrc bx = typed_rsrc<DT>(d.x, lo, kLen), bc = rsrc(d.codes + lo, kLen);
-    Raw4<DT> r[kU];
-#pragma unroll
-    for (int u = 0; u < kU; u++) r[u] = load4<DT>(bx, 4 * threadIdx.x + u * kSubTile);
-#pragma unroll
-    for (int u = 0; u < kU; u++) {
-      float x[4], s;
-      unpack4<DT>(r[u], x);
-      const uint32_t codes = block_to_codes<FMT>(x, smode, s);
-      __builtin_amdgcn_raw_buffer_store_b32(codes, bc, 4 * threadIdx.x + u * kSubTile, 0, kStPol);
-      if (lane == 0) st_global<float>(d.scale + (lo >> 7) + 8 * u + run, s);
-    }
+  // loaded with the rest of the descriptor: left to itself the compiler loads the field behind the
+  // first branch, one more wait (84.6 us against 83.8)
+  int vec = d.vec;
+  asm volatile("" : "+s"(vec));
+  if (lo + kLen <= d.numel) {
+    if (vec) quant_block_whole<true, DT, FMT>(d, lo, smode);
+    else quant_block_whole<false, DT, FMT>(d, lo, smode);
     return;
   }
   for (int u = 0; u < kU; u++) {
@@ -486,42 +503,60 @@ __global__ __launch_bounds__(kThreads) void k_quant_amax(const QuantDesc* __rest
   if (threadIdx.x == 0) amax[d.slot0 + (w - d.chunk0)] = am;
 }
 
-// Second pass: every wave takes the largest of its tensor's chunk maxima (at most
-// kAmaxMaxChunks of them, from the L2), and quantizes its share of the part.  Bound
-// by HBM: 202M bf16 values in 61 us (first pass) and 89 us (6.8 TB/s); a list past
-// the caches is read twice, since the scale needs all of a tensor.
+// The tensor's scale from its chunk maxima: at most kAmaxMaxChunks of them, one
+// 16-byte load per lane, from the L2.
+struct TensorScale {
+  vu4 maxima;
+  __device__ __forceinline__ TensorScale(const uint32_t* amax, const QuantDesc& d)
+      : maxima(__builtin_amdgcn_raw_buffer_load_b128(rsrc(amax + d.slot0, 4 * d.slots), 16 * (threadIdx.x & 63), 0, 0)) {}
+  // called by whole waves
+  template <int FMT>
+  __device__ __forceinline__ void get(int smode, float& s, float& inv, bool& odd) const {
+    const uint32_t am = wave_max(max(max(maxima.x, maxima.y), max(maxima.z, maxima.w)));
+    choose_scale_mode<FMT>(am, smode, s, inv);
+    odd = nonfinite_amax(am);
+  }
+};
+
+// The maxima are loaded first, then the values: the scale is ready when they arrive.
+template <bool DWORD, int DT, int FMT>
+__device__ __forceinline__ void quant_tensor_whole(const QuantDesc& d, int64_t lo, const TensorScale& t, int smode,
+                                                   float& s, float& inv, bool& odd) {
+  constexpr int64_t kLen = (int64_t)1 << kQuantTensorPartLog2;
+  constexpr int kU = (int)(kLen / kSubTile);
+  const Stream<DT, DWORD> sx(d.x, lo, kLen);
+  const Stream<kCodes, DWORD> sc(d.codes, lo, kLen);
+  Raw4<DT> r[kU];
+#pragma unroll
+  for (int u = 0; u < kU; u++) r[u] = sx.load(4 * threadIdx.x + u * kSubTile);
+  t.get<FMT>(smode, s, inv, odd);
+#pragma unroll
+  for (int u = 0; u < kU; u++) {
+    float x[4];
+    unpack4<DT>(r[u], x);
+    sc.store(4 * threadIdx.x + u * kSubTile, Raw4<kCodes>{codes4<FMT>(x, inv, odd)});
+  }
+}
+
+// Second pass: every wave makes its tensor's scale and quantizes its share of the
+// part.  Bound by HBM: 202M bf16 values in 61 us (first pass) and 89 us (6.8 TB/s); a
+// list past the caches is read twice, since the scale needs all of a tensor.
 template <int DT, int FMT>
 __global__ __launch_bounds__(kThreads) void k_quant_tensor(const QuantDesc* __restrict__ descs,
                                                            const int32_t* __restrict__ part_tid, int64_t nparts,
                                                            const uint32_t* __restrict__ amax, int smode) {
   constexpr int64_t kLen = (int64_t)1 << kQuantTensorPartLog2;
-  constexpr int kU = (int)(kLen / kSubTile);
   const int64_t w = run_index(nparts);
   if (w < 0) return;
   const QuantDesc d = descs[part_tid[w]];
   const int64_t lo = d.head + ((w - d.part0) << kQuantTensorPartLog2);
-  const bool whole = d.vec && lo + kLen <= d.numel;
-  // the maxima first, then the values: the scale is ready when they arrive
-  const vu4 maxima = __builtin_amdgcn_raw_buffer_load_b128(rsrc(amax + d.slot0, 4 * d.slots), 16 * (threadIdx.x & 63), 0, 0);
-  Raw4<DT> r[kU];
-  if (whole) {
-    const Rsrc bx = typed_rsrc<DT>(d.x, lo, kLen);
-#pragma unroll
-    for (int u = 0; u < kU; u++) r[u] = load4<DT>(bx, 4 * threadIdx.x + u * kSubTile);
-  }
-  const uint32_t am = wave_max(max(max(maxima.x, maxima.y), max(maxima.z, maxima.w)));
+  const bool whole = lo + kLen <= d.numel;
+  const TensorScale t(amax, d);
   float s, inv;
-  choose_scale_mode<FMT>(am, smode, s, inv);
-  const bool odd = nonfinite_amax(am);
-  if (whole) {
-    const Rsrc bc = rsrc(d.codes + lo, kLen);
-#pragma unroll
-    for (int u = 0; u < kU; u++) {
-      float x[4];
-      unpack4<DT>(r[u], x);
-      __builtin_amdgcn_raw_buffer_store_b32(codes4<FMT>(x, inv, odd), bc, 4 * threadIdx.x + u * kSubTile, 0, kStPol);
-    }
-  }
+  bool odd;
+  if (d.vec && whole) quant_tensor_whole<true, DT, FMT>(d, lo, t, smode, s, inv, odd);
+  else if (!whole) t.get<FMT>(smode, s, inv, odd);
+  else quant_tensor_whole<false, DT, FMT>(d, lo, t, smode, s, inv, odd);
   const bool first = w == d.part0;
   if (first && threadIdx.x == 0) st_global<float>(d.scale, s);
   // what is not in groups: all of another part, and the elements in front of the first
@@ -532,6 +567,29 @@ __global__ __launch_bounds__(kThreads) void k_quant_tensor(const QuantDesc* __re
   }
 }
 
+template <bool DWORD, int PL, int DT, int FMT, bool BLK>
+__device__ __forceinline__ void dequant_whole(const QuantDesc& d, int64_t lo) {
+  constexpr int64_t kLen = (int64_t)1 << PL;
+  constexpr int kU = (int)(kLen / kSubTile);
+  const Stream<DT, DWORD> sx(d.x, lo, kLen);
+  const Stream<kCodes, DWORD> sc(d.codes, lo, kLen);
+  Raw4<kCodes> c[kU];
+  float s[kU];
+#pragma unroll
+  for (int u = 0; u < kU; u++) {
+    c[u] = sc.load(4 * threadIdx.x + u * kSubTile);
+    s[u] = ld_global<float>(d.scale + (BLK ? (lo >> 7) + 8 * u + (threadIdx.x >> 5) : 0));
+  }
+#pragma unroll
+  for (int u = 0; u < kU; u++) {
+    float x[4];
+    decode4<FMT>(c[u].x, x);
+#pragma unroll
+    for (int j = 0; j < 4; j++) x[j] *= s[u];
+    sx.store(4 * threadIdx.x + u * kSubTile, pack4<DT>(x));
+  }
+}
+
 // Back to values: 109.5M E5M2 codes to fp32 in 83 us, 6.6 TB/s, bound by the writes
 // (four bytes of five).
 template <int DT, int FMT, bool BLK>
@@ -539,30 +597,13 @@ __global__ __launch_bounds__(kThreads) void k_dequant(const QuantDesc* __restric
                                                       const int32_t* __restrict__ part_tid, int64_t nparts) {
   constexpr int PL = BLK ? kQuantPartLog2 : kQuantTensorPartLog2;
   constexpr int64_t kLen = (int64_t)1 << PL;
-  constexpr int kU = (int)(kLen / kSubTile);
   const int64_t w = run_index(nparts);
   if (w < 0) return;
   const QuantDesc d = descs[part_tid[w]];
   const int64_t lo = d.head + ((w - d.part0) << PL);
-  const bool whole = d.vec && lo + kLen <= d.numel, first = w == d.part0;
-  if (whole) {
-    const Rsrc bx = typed_rsrc<DT>(d.x, lo, kLen), bc = rsrc(d.codes + lo, kLen);
-    uint32_t c[kU];
-    float s[kU];
-#pragma unroll
-    for (int u = 0; u < kU; u++) {
-      c[u] = __builtin_amdgcn_raw_buffer_load_b32(bc, 4 * threadIdx.x + u * kSubTile, 0, kLdPol);
-      s[u] = ld_global<float>(d.scale + (BLK ? (lo >> 7) + 8 * u + (threadIdx.x >> 5) : 0));
-    }
-#pragma unroll
-    for (int u = 0; u < kU; u++) {
-      float x[4];
-      decode4<FMT>(c[u], x);
-#pragma unroll
-      for (int j = 0; j < 4; j++) x[j] *= s[u];
-      store4<DT>(bx, 4 * threadIdx.x + u * kSubTile, x);
-    }
-  }
+  const bool whole = lo + kLen <= d.numel, first = w == d.part0;
+  if (d.vec && whole) dequant_whole<true, PL, DT, FMT, BLK>(d, lo);
+  else if (whole) dequant_whole<false, PL, DT, FMT, BLK>(d, lo);
   const int64_t from = first ? 0 : lo, to = whole ? first ? (int64_t)d.head : lo : min(lo + kLen, d.numel);
   for (int64_t i = from + threadIdx.x; i < to; i += kThreads)
     st_elem<DT>(d.x, i, decode1<FMT>(ld_global<uint8_t>(d.codes + i)) * ld_global<float>(d.scale + (BLK ? i >> 7 : 0)));
@@ -898,7 +939,7 @@ int adamw_plan(fp8adam_plan** out, const fp8adam_adamw_tensor* T, int32_t n, con
     const fp8adam_adamw_tensor& x = T[t];
     grads[t] = GradDesc{x.grad, nullptr, x.numel, 0, x.grad_dtype, 0};
     const bool s8 = x.moments == FP8ADAM_MOMENTS_8;
-    desc[t] = AdamwDesc{x.param, x.grad, x.copy, x.m, x.v, x.m_scale, x.v_scale, x.numel, 0, x.group, 0, 0};
+    desc[t] = AdamwDesc{x.param, x.grad, x.copy, x.m, x.v, x.m_scale, x.v_scale, x.numel, 0, x.group, 0, 0, 0};
     if (x.numel == 0) continue;
     const AdamwKind kind{x.param_dtype, x.copy ? x.copy_dtype : 0, x.grad_dtype, s8};
     // Streams that start on dwords: fp32 ones always do; 16-bit ones with 32-bit moments either at
