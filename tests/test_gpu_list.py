@@ -767,6 +767,29 @@ def test_amp_state_goes_as_in_the_fp8_step():
     b.close()
 
 
+@pytest.mark.parametrize("chunks", [1, 2, 9, 63, 64, 65, 600])
+def test_amp_norm_of_every_call(chunks):
+    """Lists on both sides of the one-launch rule (64 chunks of 4096): the norm of every call is that
+    call's, whichever work-group ends last; the same gradients give the same bits."""
+    g = gen(chunks)
+    n = 4096 * chunks - 5
+    gr = torch.zeros(n, device="cuda", dtype=BF16)
+    opt = pk.AdamW([torch.zeros(n, device="cuda")], [gr])
+    amp = pk.amp_state(1.0)
+    base = torch.randn(n, generator=g, device="cuda").bfloat16()
+    norm = math.sqrt(float(base.double().square().sum()))
+    seen = {}
+    for call in range(60):
+        k = call % 5
+        torch.mul(base, 2.0 ** k, out=gr)  # exact: a power of two
+        opt.step_amp(amp, max_norm=1.0, growth_interval=10 ** 6, **HP)
+        got = amp_fields(amp)["grad_norm"]
+        assert abs(got - norm * 2.0 ** k) <= 2 * U * norm * 2.0 ** k, (call, got)
+        assert seen.setdefault(k, got) == got
+    assert amp_fields(amp)["step"] == 60
+    opt.close()
+
+
 def test_amp_over_every_kind_in_one_list():
     """One norm over gradients of three types, then every kind of tensor with the same factor."""
     g = gen(15)
