@@ -35,6 +35,9 @@ int fail(int code, const std::string& msg) {
 }
 
 int hip_fail(hipError_t e, const char* what) {
+  // the runtime keeps the error as the thread's last one, through later calls that succeed:
+  // it is reported here and must not be found by whoever asks next
+  (void)hipGetLastError();
   return fail(FP8ADAM_EHIP, std::string(what) + ": " + hipGetErrorString(e));
 }
 

@@ -1598,6 +1598,21 @@ int hip_fail(hipError_t e, const char* what);
 
 
 
+// Launch a kernel with the argument conversions of hipLaunchKernelGGL, judged by the
+// launch's own result: the thread's last error may be that of any earlier call.
+template <typename... Formals, typename... Actuals>
+inline int launch(void (*kernel)(Formals...), dim3 grid, dim3 block, unsigned lds, hipStream_t s, Actuals... actuals) {
+  static_assert(sizeof...(Formals) == sizeof...(Actuals), "kernel argument count");
+  std::tuple<Formals...> formals{actuals...};
+  void* argv[sizeof...(Formals)];
+  std::apply([&argv](auto&... f) {
+    int i = 0;
+    ((argv[i++] = static_cast<void*>(&f)), ...);
+  }, formals);
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, argv, lds, s);
+  return e == hipSuccess ? 0 : hip_fail(e, "kernel launch");
+}
+
 #define HIP_TRY(expr)                                    \
   do {                                                   \
     hipError_t e_ = (expr);                              \

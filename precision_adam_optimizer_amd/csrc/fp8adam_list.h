@@ -482,31 +482,31 @@ struct AdamwKind {
 };
 
 template <int PD, int CD, int GD, bool S8, int MF, int VF>
-inline void launch_adamw_kind(const AdamwDesc* descs, const int32_t* part_tid, const AdamwConsts& C, int64_t nparts,
-                              const AdamwCtl* ctl, hipStream_t s) {
+inline int launch_adamw_kind(const AdamwDesc* descs, const int32_t* part_tid, const AdamwConsts& C, int64_t nparts,
+                             const AdamwCtl* ctl, hipStream_t s) {
   // 32-bit moments: five work-groups on a CU.  842M fp32 weights with a copy 3.96 ms against 4.09 with
   // eight (four: 3.98, three: 4.03), without one 3.59 against 3.73; 109.5M with a copy 507 us against 519
   // (four: 525); 842M bf16 weights 3.04 ms against 3.06.  8-bit moments read more than they write: they lose.
-  hipLaunchKernelGGL((k_adamw<PD, CD, GD, S8, MF, VF>), dim3(run_grid(nparts)), dim3(kThreads), lds_for(S8 ? 8 : 5), s,
-                     descs, part_tid, C, nparts, ctl);
+  return launch(k_adamw<PD, CD, GD, S8, MF, VF>, dim3(run_grid(nparts)), dim3(kThreads), lds_for(S8 ? 8 : 5), s, descs,
+                part_tid, C, nparts, ctl);
 }
 
-// The launch of one kind's parts (the caller checks the launch).
+// The launch of one kind's parts.
 template <bool S8, int MF, int VF>
-void launch_adamw(const AdamwKind& k, const AdamwDesc* descs, const int32_t* part_tid, const AdamwConsts& C,
-                  int64_t nparts, const AdamwCtl* ctl, hipStream_t s) {
-  auto by_grad = [&](auto pd, auto cd) {
+int launch_adamw(const AdamwKind& k, const AdamwDesc* descs, const int32_t* part_tid, const AdamwConsts& C,
+                 int64_t nparts, const AdamwCtl* ctl, hipStream_t s) {
+  auto by_grad = [&](auto pd, auto cd) -> int {
     constexpr int P = decltype(pd)::value, Y = decltype(cd)::value;
-    if (k.g == FP8ADAM_F32) launch_adamw_kind<P, Y, FP8ADAM_F32, S8, MF, VF>(descs, part_tid, C, nparts, ctl, s);
-    else if (k.g == FP8ADAM_BF16) launch_adamw_kind<P, Y, FP8ADAM_BF16, S8, MF, VF>(descs, part_tid, C, nparts, ctl, s);
-    else launch_adamw_kind<P, Y, FP8ADAM_F16, S8, MF, VF>(descs, part_tid, C, nparts, ctl, s);
+    if (k.g == FP8ADAM_F32) return launch_adamw_kind<P, Y, FP8ADAM_F32, S8, MF, VF>(descs, part_tid, C, nparts, ctl, s);
+    if (k.g == FP8ADAM_BF16) return launch_adamw_kind<P, Y, FP8ADAM_BF16, S8, MF, VF>(descs, part_tid, C, nparts, ctl, s);
+    return launch_adamw_kind<P, Y, FP8ADAM_F16, S8, MF, VF>(descs, part_tid, C, nparts, ctl, s);
   };
   using std::integral_constant;
-  if (k.p == FP8ADAM_BF16) by_grad(integral_constant<int, FP8ADAM_BF16>{}, integral_constant<int, 0>{});
-  else if (k.p == FP8ADAM_F16) by_grad(integral_constant<int, FP8ADAM_F16>{}, integral_constant<int, 0>{});
-  else if (k.copy == FP8ADAM_BF16) by_grad(integral_constant<int, FP8ADAM_F32>{}, integral_constant<int, FP8ADAM_BF16>{});
-  else if (k.copy == FP8ADAM_F16) by_grad(integral_constant<int, FP8ADAM_F32>{}, integral_constant<int, FP8ADAM_F16>{});
-  else by_grad(integral_constant<int, FP8ADAM_F32>{}, integral_constant<int, 0>{});
+  if (k.p == FP8ADAM_BF16) return by_grad(integral_constant<int, FP8ADAM_BF16>{}, integral_constant<int, 0>{});
+  if (k.p == FP8ADAM_F16) return by_grad(integral_constant<int, FP8ADAM_F16>{}, integral_constant<int, 0>{});
+  if (k.copy == FP8ADAM_BF16) return by_grad(integral_constant<int, FP8ADAM_F32>{}, integral_constant<int, FP8ADAM_BF16>{});
+  if (k.copy == FP8ADAM_F16) return by_grad(integral_constant<int, FP8ADAM_F32>{}, integral_constant<int, FP8ADAM_F16>{});
+  return by_grad(integral_constant<int, FP8ADAM_F32>{}, integral_constant<int, 0>{});
 }
 
 }  // namespace fp8adam_list

@@ -14,16 +14,16 @@ using namespace fp8adam_list;
 
 namespace fp8adam_list {
 
-extern template void launch_adamw<false, 0, 0>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
-                                               int64_t, const AdamwCtl*, hipStream_t);
-extern template void launch_adamw<true, 0, 1>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
+extern template int launch_adamw<false, 0, 0>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
                                               int64_t, const AdamwCtl*, hipStream_t);
-extern template void launch_adamw<true, 0, 0>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
-                                              int64_t, const AdamwCtl*, hipStream_t);
-extern template void launch_adamw<true, 1, 0>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
-                                              int64_t, const AdamwCtl*, hipStream_t);
-extern template void launch_adamw<true, 1, 1>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
-                                              int64_t, const AdamwCtl*, hipStream_t);
+extern template int launch_adamw<true, 0, 1>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
+                                             int64_t, const AdamwCtl*, hipStream_t);
+extern template int launch_adamw<true, 0, 0>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
+                                             int64_t, const AdamwCtl*, hipStream_t);
+extern template int launch_adamw<true, 1, 0>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
+                                             int64_t, const AdamwCtl*, hipStream_t);
+extern template int launch_adamw<true, 1, 1>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&,
+                                             int64_t, const AdamwCtl*, hipStream_t);
 
 namespace {
 
@@ -730,7 +730,10 @@ struct Image {
   }
   int upload(fp8adam_plan* p, hipStream_t stream) {
     hipError_t e = hipMalloc((void**)&p->mem, std::max<size_t>(size, 256));
-    if (e == hipErrorOutOfMemory) return fail(FP8ADAM_ENOMEM, "device allocation failed");
+    if (e == hipErrorOutOfMemory) {
+      (void)hip_fail(e, "hipMalloc");  // (takes the error from the runtime)
+      return fail(FP8ADAM_ENOMEM, "device allocation failed");
+    }
     if (e == hipSuccess && !bytes.empty())
       e = hipMemcpyAsync(p->mem, bytes.data(), bytes.size(), hipMemcpyHostToDevice, stream);
     if (e == hipSuccess) e = hipStreamSynchronize(stream);
@@ -772,21 +775,22 @@ void chunk_grads(std::vector<GradDesc>& g, int64_t total, int& chunk_log2, std::
   }
 }
 
-void launch_sumsq(const fp8adam_plan* p, hipStream_t s) {
-  if (p->grad_chunks)
-    hipLaunchKernelGGL(k_list_sumsq, dim3((unsigned)p->norm_groups()), dim3(kThreads), 0, s, p->d_grad, p->d_grad_tid,
-                       p->grad_chunks, p->grad_chunk_log2, p->d_partial);
+int launch_sumsq(const fp8adam_plan* p, hipStream_t s) {
+  if (!p->grad_chunks) return 0;
+  return launch(k_list_sumsq, dim3((unsigned)p->norm_groups()), dim3(kThreads), 0, s, p->d_grad, p->d_grad_tid,
+                p->grad_chunks, p->grad_chunk_log2, p->d_partial);
 }
 
 int run_adamw(fp8adam_plan* p, const AdamwConsts& C, const AdamwCtl* ctl, hipStream_t s) {
   const AdamwDesc* d = static_cast<const AdamwDesc*>(p->d_desc);
   for (const Span& k : p->spans) {
-    if (!k.kind.moments8) launch_adamw<false, 0, 0>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
-    else if (p->mf == 0 && p->vf == 1) launch_adamw<true, 0, 1>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
-    else if (p->mf == 0) launch_adamw<true, 0, 0>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
-    else if (p->vf == 0) launch_adamw<true, 1, 0>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
-    else launch_adamw<true, 1, 1>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
-    HIP_TRY(hipGetLastError());
+    int r;
+    if (!k.kind.moments8) r = launch_adamw<false, 0, 0>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
+    else if (p->mf == 0 && p->vf == 1) r = launch_adamw<true, 0, 1>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
+    else if (p->mf == 0) r = launch_adamw<true, 0, 0>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
+    else if (p->vf == 0) r = launch_adamw<true, 1, 0>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
+    else r = launch_adamw<true, 1, 1>(k.kind, d, k.d_tid, C, k.nparts, ctl, s);
+    if (r) return r;
   }
   return 0;
 }
@@ -830,15 +834,10 @@ template <int DT, int FMT>
 int run_quantize(fp8adam_plan* p, const Span& k, hipStream_t s) {
   const QuantDesc* d = static_cast<const QuantDesc*>(p->d_desc);
   const dim3 grid(run_grid(k.nparts));
-  if (p->granularity == FP8ADAM_SCALE_BLOCK128) {
-    hipLaunchKernelGGL((k_quant_block<DT, FMT>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts, p->smode);
-  } else {
-    hipLaunchKernelGGL((k_quant_amax<DT>), dim3((unsigned)k.nchunks), dim3(kThreads), 0, s, d, k.d_ctid, p->d_amax);
-    HIP_TRY(hipGetLastError());
-    hipLaunchKernelGGL((k_quant_tensor<DT, FMT>), grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts, p->d_amax, p->smode);
-  }
-  HIP_TRY(hipGetLastError());
-  return 0;
+  if (p->granularity == FP8ADAM_SCALE_BLOCK128)
+    return launch(k_quant_block<DT, FMT>, grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts, p->smode);
+  if (int r = launch(k_quant_amax<DT>, dim3((unsigned)k.nchunks), dim3(kThreads), 0, s, d, k.d_ctid, p->d_amax)) return r;
+  return launch(k_quant_tensor<DT, FMT>, grid, dim3(kThreads), 0, s, d, k.d_tid, k.nparts, p->d_amax, p->smode);
 }
 
 // Dequantizing writes four bytes of five (two of three): as many work-groups on a CU
@@ -855,13 +854,9 @@ int run_dequantize(fp8adam_plan* p, const Span& k, hipStream_t s) {
   const QuantDesc* d = static_cast<const QuantDesc*>(p->d_desc);
   const dim3 grid(run_grid(k.nparts));
   if (p->granularity == FP8ADAM_SCALE_BLOCK128)
-    hipLaunchKernelGGL((k_dequant<DT, FMT, true>), grid, dim3(kThreads), dequant_lds(kQuantPartLog2, DT), s, d, k.d_tid,
-                       k.nparts);
-  else
-    hipLaunchKernelGGL((k_dequant<DT, FMT, false>), grid, dim3(kThreads), dequant_lds(kQuantTensorPartLog2, DT), s, d,
-                       k.d_tid, k.nparts);
-  HIP_TRY(hipGetLastError());
-  return 0;
+    return launch(k_dequant<DT, FMT, true>, grid, dim3(kThreads), dequant_lds(kQuantPartLog2, DT), s, d, k.d_tid, k.nparts);
+  return launch(k_dequant<DT, FMT, false>, grid, dim3(kThreads), dequant_lds(kQuantTensorPartLog2, DT), s, d, k.d_tid,
+                k.nparts);
 }
 
 template <int FMT>
@@ -1208,14 +1203,14 @@ int fp8adam_adamw_step_amp(fp8adam_plan* plan, const fp8adam_adamw_hparams* grou
       a.R.v_scale[q] = sc * sc;
     }
     if (plan->grad_chunks > 0 && plan->grad_chunks <= kTicketGroups) {
-      hipLaunchKernelGGL(k_list_sumsq_ctl, dim3((unsigned)plan->grad_chunks), dim3(kThreads), 0, stream, plan->d_grad,
-                         plan->d_grad_tid, plan->grad_chunks, plan->grad_chunk_log2, plan->d_partial, plan->d_ticket, a);
+      if (int r = launch(k_list_sumsq_ctl, dim3((unsigned)plan->grad_chunks), dim3(kThreads), 0, stream, plan->d_grad,
+                         plan->d_grad_tid, plan->grad_chunks, plan->grad_chunk_log2, plan->d_partial, plan->d_ticket, a))
+        return r;
     } else {
-      launch_sumsq(plan, stream);
-      HIP_TRY(hipGetLastError());
-      hipLaunchKernelGGL(k_list_ctl, dim3(1), dim3(kThreads), 0, stream, plan->d_partial, plan->norm_groups(), a);
+      if (int r = launch_sumsq(plan, stream)) return r;
+      if (int r = launch(k_list_ctl, dim3(1), dim3(kThreads), 0, stream, plan->d_partial, plan->norm_groups(), a))
+        return r;
     }
-    HIP_TRY(hipGetLastError());
     return run_adamw(plan, C, plan->d_ctl, stream);
   });
 }
@@ -1226,13 +1221,10 @@ int fp8adam_clip_grads(fp8adam_plan* plan, float max_norm, float* result, hipStr
     if (!isfinite(max_norm)) return fail(FP8ADAM_EINVAL, "max_norm must be finite");
     if (!result) return fail(FP8ADAM_EINVAL, "result is null");
     if ((uintptr_t)result & 3u) return fail(FP8ADAM_EALIGN, "result is not 4-byte aligned");
-    launch_sumsq(plan, stream);
-    HIP_TRY(hipGetLastError());
-    hipLaunchKernelGGL(k_list_clip, dim3(run_grid<kClipXcdRun>(std::max<int64_t>(1, plan->clip_parts))), dim3(kThreads),
-                       0, stream, plan->d_grad, plan->d_grad_tid, plan->clip_parts, plan->grad_chunk_log2, plan->d_partial,
-                       plan->norm_groups(), max_norm, result);
-    HIP_TRY(hipGetLastError());
-    return 0;
+    if (int r = launch_sumsq(plan, stream)) return r;
+    return launch(k_list_clip, dim3(run_grid<kClipXcdRun>(std::max<int64_t>(1, plan->clip_parts))), dim3(kThreads), 0,
+                  stream, plan->d_grad, plan->d_grad_tid, plan->clip_parts, plan->grad_chunk_log2, plan->d_partial,
+                  plan->norm_groups(), max_norm, result);
   });
 }
 

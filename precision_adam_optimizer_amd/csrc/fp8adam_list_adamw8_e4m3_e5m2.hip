@@ -4,7 +4,7 @@
 
 namespace fp8adam_list {
 
-template void launch_adamw<true, 0, 1>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&, int64_t,
-                                         const AdamwCtl*, hipStream_t);
+template int launch_adamw<true, 0, 1>(const AdamwKind&, const AdamwDesc*, const int32_t*, const AdamwConsts&, int64_t,
+                                        const AdamwCtl*, hipStream_t);
 
 }  // namespace fp8adam_list
