@@ -498,15 +498,15 @@ void free_ctx(fp8adam_ctx* c) {
 
 int64_t norm_groups(const fp8adam_ctx* c) { return std::min<int64_t>(c->nchunks, kNormGroups); }
 
-void launch_gradnorm(fp8adam_ctx* c, hipStream_t s) {
-  launch_k(c, k_gradnorm, dim3((unsigned)norm_groups(c)), dim3(kThreads), s, descs_of(c, c->cur), c->d_chunk_tid,
-           c->d_gpart, c->chunk_log2, c->nchunks);
+int launch_gradnorm(fp8adam_ctx* c, hipStream_t s) {
+  return launch_k(c, k_gradnorm, dim3((unsigned)norm_groups(c)), dim3(kThreads), s, descs_of(c, c->cur), c->d_chunk_tid,
+                  c->d_gpart, c->chunk_log2, c->nchunks);
 }
 
-void launch_gradctl(fp8adam_ctx* c, const fp8adam_amp_config& amp, fp8adam_amp_state* state,
-                    const fp8adam_hparams& hp, hipStream_t s) {
-  launch_k(c, k_gradctl, dim3(1), dim3(kReduceThreads), s, c->d_gpart, norm_groups(c), state, c->d_gctl, amp, hp.lr,
-           hp.beta1, hp.beta2, c->hist_len);
+int launch_gradctl(fp8adam_ctx* c, const fp8adam_amp_config& amp, fp8adam_amp_state* state,
+                   const fp8adam_hparams& hp, hipStream_t s) {
+  return launch_k(c, k_gradctl, dim3(1), dim3(kReduceThreads), s, c->d_gpart, norm_groups(c), state, c->d_gctl, amp, hp.lr,
+                  hp.beta1, hp.beta2, c->hist_len);
 }
 
 int run_step(fp8adam_ctx* c, const StepConsts& k, int64_t t, hipStream_t s) {
@@ -736,19 +736,20 @@ int fp8adam_init(fp8adam_ctx** out, const fp8adam_tensor* tensors, int32_t n, co
         e = hipMemsetAsync(tensors[t].m, 0, (size_t)tensors[t].numel, stream);
         if (e == hipSuccess) e = hipMemsetAsync(tensors[t].v, 0, (size_t)tensors[t].numel, stream);
       }
-      if (e == hipSuccess) {
-        hipLaunchKernelGGL(k_fresh_state, dim3((unsigned)n), dim3(kThreads), 0, stream, c->d_desc,
-                           cfg->granularity == FP8ADAM_SCALE_BLOCK128 ? 1 : 0, 2 * c->hist_len);
-        e = hipGetLastError();
-      }
+      if (e == hipSuccess)
+        if (int r = launch(k_fresh_state, dim3((unsigned)n), dim3(kThreads), 0, stream, c->d_desc,
+                           cfg->granularity == FP8ADAM_SCALE_BLOCK128 ? 1 : 0, 2 * c->hist_len)) {
+          free_ctx(c);
+          return r;
+        }
     }
     if (e == hipSuccess)
       e = hipMemsetAsync(c->d_counters, 0, sizeof(unsigned long long) * (size_t)n * kStatsPerTensor, stream);
     if (e == hipSuccess) e = hipStreamSynchronize(stream);
     if (e != hipSuccess) {
       free_ctx(c);
-      return e == hipErrorOutOfMemory ? fail(FP8ADAM_ENOMEM, "device allocation failed")
-                                      : hip_fail(e, "fp8adam_init");
+      const int r = hip_fail(e, "fp8adam_init");  // (takes the error from the runtime)
+      return e == hipErrorOutOfMemory ? fail(FP8ADAM_ENOMEM, "device allocation failed") : r;
     }
     *out = c;
     return 0;
@@ -835,7 +836,6 @@ int fp8adam_step_amp(fp8adam_ctx* ctx, const fp8adam_hparams* hp, const fp8adam_
     hipStream_t s = stream;
     if (c->nchunks > 0) TIMED(10, launch_gradnorm(c, s));
     TIMED(11, (launch_gradctl(c, *amp, state, *hp, s)));
-    HIP_TRY(hipGetLastError());
     c->gctl = c->d_gctl;
     const int r = run_step(c, k, hp->step, s);
     c->gctl = nullptr;
@@ -913,9 +913,9 @@ int fp8adam_step_noalloc(const fp8adam_tensor* tensors, int32_t n, const fp8adam
                             T.numel, chunk0, nullptr};
         chunk0 += (T.numel + ((int64_t)1 << chunk_log2) - 1) >> chunk_log2;
       }
-      hipLaunchKernelGGL(k_noalloc_setup, dim3((unsigned)b.count), dim3(kThreads), 0, stream, b, c.d_desc,
-                         c.d_chunk_tid, chunk_log2);
-      HIP_TRY(hipGetLastError());
+      if (int r = launch(k_noalloc_setup, dim3((unsigned)b.count), dim3(kThreads), 0, stream, b, c.d_desc, c.d_chunk_tid,
+                         chunk_log2))
+        return r;
     }
     return run_step(&c, k, hp->step, stream);
   } catch (...) {
@@ -1038,22 +1038,16 @@ int fp8adam_encode(int32_t fmt, const float* x, uint8_t* out, int64_t n, hipStre
   if (!valid_fmt(fmt) || n < 0 || (n > 0 && (!x || !out))) return fail(FP8ADAM_EINVAL, "bad argument");
   if (n == 0) return 0;
   if (fmt == 0)
-    hipLaunchKernelGGL(k_encode<0>, dim3(probe_grid(n, 4)), dim3(kThreads), 0, stream, x, out, n);
-  else
-    hipLaunchKernelGGL(k_encode<1>, dim3(probe_grid(n, 4)), dim3(kThreads), 0, stream, x, out, n);
-  HIP_TRY(hipGetLastError());
-  return 0;
+    return launch(k_encode<0>, dim3(probe_grid(n, 4)), dim3(kThreads), 0, stream, x, out, n);
+  return launch(k_encode<1>, dim3(probe_grid(n, 4)), dim3(kThreads), 0, stream, x, out, n);
 }
 
 int fp8adam_decode(int32_t fmt, const uint8_t* codes, float* out, int64_t n, hipStream_t stream) {
   if (!valid_fmt(fmt) || n < 0 || (n > 0 && (!codes || !out))) return fail(FP8ADAM_EINVAL, "bad argument");
   if (n == 0) return 0;
   if (fmt == 0)
-    hipLaunchKernelGGL(k_decode<0>, dim3(probe_grid(n, 1)), dim3(kThreads), 0, stream, codes, out, n);
-  else
-    hipLaunchKernelGGL(k_decode<1>, dim3(probe_grid(n, 1)), dim3(kThreads), 0, stream, codes, out, n);
-  HIP_TRY(hipGetLastError());
-  return 0;
+    return launch(k_decode<0>, dim3(probe_grid(n, 1)), dim3(kThreads), 0, stream, codes, out, n);
+  return launch(k_decode<1>, dim3(probe_grid(n, 1)), dim3(kThreads), 0, stream, codes, out, n);
 }
 
 int fp8adam_encode_sr_bits_range(int32_t fmt, uint32_t start, int64_t count, uint32_t r16, uint8_t* out,
@@ -1063,13 +1057,10 @@ int fp8adam_encode_sr_bits_range(int32_t fmt, uint32_t start, int64_t count, uin
     return fail(FP8ADAM_EINVAL, "bad argument");
   if (count == 0) return 0;
   if (fmt == 0)
-    hipLaunchKernelGGL(k_encode_sr_bits<0>, dim3(probe_grid(count, 4)), dim3(kThreads), 0, stream, start, count, r16,
-                       out);
-  else
-    hipLaunchKernelGGL(k_encode_sr_bits<1>, dim3(probe_grid(count, 4)), dim3(kThreads), 0, stream, start, count, r16,
-                       out);
-  HIP_TRY(hipGetLastError());
-  return 0;
+    return launch(k_encode_sr_bits<0>, dim3(probe_grid(count, 4)), dim3(kThreads), 0, stream, start, count, r16,
+                  out);
+  return launch(k_encode_sr_bits<1>, dim3(probe_grid(count, 4)), dim3(kThreads), 0, stream, start, count, r16,
+                  out);
 }
 
 int fp8adam_encode_sr(int32_t fmt, const float* x, const uint16_t* r16, uint8_t* out, int64_t n,
@@ -1077,11 +1068,8 @@ int fp8adam_encode_sr(int32_t fmt, const float* x, const uint16_t* r16, uint8_t*
   if (!valid_fmt(fmt) || n < 0 || (n > 0 && (!x || !r16 || !out))) return fail(FP8ADAM_EINVAL, "bad argument");
   if (n == 0) return 0;
   if (fmt == 0)
-    hipLaunchKernelGGL(k_encode_sr<0>, dim3(probe_grid(n, 1)), dim3(kThreads), 0, stream, x, r16, out, n);
-  else
-    hipLaunchKernelGGL(k_encode_sr<1>, dim3(probe_grid(n, 1)), dim3(kThreads), 0, stream, x, r16, out, n);
-  HIP_TRY(hipGetLastError());
-  return 0;
+    return launch(k_encode_sr<0>, dim3(probe_grid(n, 1)), dim3(kThreads), 0, stream, x, r16, out, n);
+  return launch(k_encode_sr<1>, dim3(probe_grid(n, 1)), dim3(kThreads), 0, stream, x, r16, out, n);
 }
 
 int fp8adam_stream_copy(const void* src, void* dst, int64_t bytes, hipStream_t stream) {
@@ -1092,10 +1080,8 @@ int fp8adam_stream_copy(const void* src, void* dst, int64_t bytes, hipStream_t s
   const int64_t n16 = bytes / 16;
   const int64_t groups = (n16 + 4 * kThreads - 1) / (4 * kThreads);
   if (groups > (int64_t)INT32_MAX) return fail(FP8ADAM_EINVAL, "copy too large");
-  hipLaunchKernelGGL(k_stream_copy, dim3((unsigned)groups), dim3(kThreads), 0, stream, static_cast<const vu4*>(src),
-                     static_cast<vu4*>(dst), n16);
-  HIP_TRY(hipGetLastError());
-  return 0;
+  return launch(k_stream_copy, dim3((unsigned)groups), dim3(kThreads), 0, stream, static_cast<const vu4*>(src),
+                static_cast<vu4*>(dst), n16);
 }
 
 int fp8adam_stream_rw(const void* src, int64_t read_bytes, void* dst, int64_t write_bytes, hipStream_t stream) {
@@ -1107,10 +1093,8 @@ int fp8adam_stream_rw(const void* src, int64_t read_bytes, void* dst, int64_t wr
   const int64_t groups = (std::max(n_read, n_write) + 4 * kThreads - 1) / (4 * kThreads);
   if (groups > (int64_t)INT32_MAX) return fail(FP8ADAM_EINVAL, "stream too large");
   if (groups == 0) return 0;
-  hipLaunchKernelGGL(k_stream_rw, dim3((unsigned)groups), dim3(kThreads), 0, stream, static_cast<const vu4*>(src),
-                     n_read, static_cast<vu4*>(dst), n_write);
-  HIP_TRY(hipGetLastError());
-  return 0;
+  return launch(k_stream_rw, dim3((unsigned)groups), dim3(kThreads), 0, stream, static_cast<const vu4*>(src),
+                n_read, static_cast<vu4*>(dst), n_write);
 }
 
 int fp8adam_stream_mix(int32_t master, void* p, const void* g, const void* m_in, const void* v_in, void* m_out,
@@ -1132,13 +1116,10 @@ int fp8adam_stream_mix(int32_t master, void* p, const void* g, const void* m_in,
   auto* mo = static_cast<uint8_t*>(m_out);
   auto* vo = static_cast<uint8_t*>(v_out);
   if (bf16)
-    hipLaunchKernelGGL(k_stream_mix<true>, dim3(grid_for<kXcdStreams>(nparts)), dim3(kThreads), 0, stream, p, gg, mi, vi,
-                       mo, vo, nparts);
-  else
-    hipLaunchKernelGGL(k_stream_mix<false>, dim3(grid_for<kXcdStreams>(nparts)), dim3(kThreads), 0, stream, p, gg, mi,
-                       vi, mo, vo, nparts);
-  HIP_TRY(hipGetLastError());
-  return 0;
+    return launch(k_stream_mix<true>, dim3(grid_for<kXcdStreams>(nparts)), dim3(kThreads), 0, stream, p, gg, mi, vi,
+                  mo, vo, nparts);
+  return launch(k_stream_mix<false>, dim3(grid_for<kXcdStreams>(nparts)), dim3(kThreads), 0, stream, p, gg, mi,
+                  vi, mo, vo, nparts);
 }
 
 int fp8adam_encode_bits_range(int32_t fmt, uint32_t start, int64_t count, uint8_t* out, hipStream_t stream) {
@@ -1146,11 +1127,8 @@ int fp8adam_encode_bits_range(int32_t fmt, uint32_t start, int64_t count, uint8_
     return fail(FP8ADAM_EINVAL, "bad argument");
   if (count == 0) return 0;
   if (fmt == 0)
-    hipLaunchKernelGGL(k_encode_bits<0>, dim3(probe_grid(count, 4)), dim3(kThreads), 0, stream, start, count, out);
-  else
-    hipLaunchKernelGGL(k_encode_bits<1>, dim3(probe_grid(count, 4)), dim3(kThreads), 0, stream, start, count, out);
-  HIP_TRY(hipGetLastError());
-  return 0;
+    return launch(k_encode_bits<0>, dim3(probe_grid(count, 4)), dim3(kThreads), 0, stream, start, count, out);
+  return launch(k_encode_bits<1>, dim3(probe_grid(count, 4)), dim3(kThreads), 0, stream, start, count, out);
 }
 
 }  // extern "C"

@@ -1598,10 +1598,11 @@ int hip_fail(hipError_t e, const char* what);
 
 
 
-// Launch a kernel with the argument conversions of hipLaunchKernelGGL, judged by the
-// launch's own result: the thread's last error may be that of any earlier call.
-template <typename... Formals, typename... Actuals>
-inline int launch(void (*kernel)(Formals...), dim3 grid, dim3 block, unsigned lds, hipStream_t s, Actuals... actuals) {
+// A kernel's arguments, converted as hipLaunchKernelGGL converts them, handed as an array of
+// pointers to `run`.  A launch is judged by its own result: the thread's last error may be that
+// of any earlier call.
+template <typename F, typename... Formals, typename... Actuals>
+inline int launch_with(F&& run, void (*kernel)(Formals...), Actuals... actuals) {
   static_assert(sizeof...(Formals) == sizeof...(Actuals), "kernel argument count");
   std::tuple<Formals...> formals{actuals...};
   void* argv[sizeof...(Formals)];
@@ -1609,8 +1610,14 @@ inline int launch(void (*kernel)(Formals...), dim3 grid, dim3 block, unsigned ld
     int i = 0;
     ((argv[i++] = static_cast<void*>(&f)), ...);
   }, formals);
-  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, argv, lds, s);
+  const hipError_t e = run(reinterpret_cast<const void*>(kernel), argv);
   return e == hipSuccess ? 0 : hip_fail(e, "kernel launch");
+}
+
+template <typename... Formals, typename... Actuals>
+inline int launch(void (*kernel)(Formals...), dim3 grid, dim3 block, unsigned lds, hipStream_t s, Actuals... actuals) {
+  return launch_with([&](const void* fn, void** argv) { return hipLaunchKernel(fn, grid, block, argv, lds, s); }, kernel,
+                     actuals...);
 }
 
 #define HIP_TRY(expr)                                    \
@@ -1693,26 +1700,19 @@ inline int timed_end(fp8adam_ctx* c, int slot, hipStream_t) {
   return 0;
 }
 
-// Launch a kernel with the argument conversions of hipLaunchKernelGGL; inside a
-// timed launch through hipExtLaunchKernel with the pending slot's events.
+// Launch a kernel; inside a timed launch through hipExtLaunchKernel with the
+// pending slot's events (a launch that fails gives the slot back).
 template <typename... Formals, typename... Actuals>
-inline void launch_k(fp8adam_ctx* c, void (*kernel)(Formals...), dim3 grid, dim3 block, hipStream_t s,
-                     Actuals... actuals) {
-  static_assert(sizeof...(Formals) == sizeof...(Actuals), "kernel argument count");
-  std::tuple<Formals...> formals{actuals...};
-  void* argv[sizeof...(Formals) > 0 ? sizeof...(Formals) : 1];
-  std::apply([&argv](auto&... f) {
-    int i = 0;
-    ((argv[i++] = static_cast<void*>(&f)), ...);
-  }, formals);
-  const void* fn = reinterpret_cast<const void*>(kernel);
-  if (c->ev_pending >= 0) {
-    const int slot = c->ev_pending;
-    c->ev_pending = -1;
-    (void)hipExtLaunchKernel(fn, grid, block, argv, 0, s, c->ev[2 * slot], c->ev[2 * slot + 1], 0);
-  } else {
-    (void)hipLaunchKernel(fn, grid, block, argv, 0, s);
-  }
+inline int launch_k(fp8adam_ctx* c, void (*kernel)(Formals...), dim3 grid, dim3 block, hipStream_t s,
+                    Actuals... actuals) {
+  const int slot = c->ev_pending;
+  if (slot < 0) return launch(kernel, grid, block, 0u, s, actuals...);
+  c->ev_pending = -1;
+  const int r = launch_with([&](const void* fn, void** argv) {
+    return hipExtLaunchKernel(fn, grid, block, argv, 0, s, c->ev[2 * slot], c->ev[2 * slot + 1], 0);
+  }, kernel, actuals...);
+  if (r) c->ev_used--;
+  return r;
 }
 
 // ---- kernel dispatch over the template parameters ----
@@ -1720,91 +1720,91 @@ inline void launch_k(fp8adam_ctx* c, void (*kernel)(Formals...), dim3 grid, dim3
 inline const TensorDesc* descs_of(const fp8adam_ctx* c, int which) { return c->d_desc + (size_t)which * c->n; }
 
 template <int MF, int VF, bool BF16P, bool L2>
-void launch_amax(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
-  launch_k(c, k_amax<MF, VF, BF16P && L2, L2>, dim3(grid_for<false>(c->nchunks)), dim3(kThreads), s, descs_of(c, c->cur),
-           c->d_chunk_tid, c->d_partial, k, c->chunk_log2, c->nchunks, c->gctl);
+int launch_amax(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
+  return launch_k(c, k_amax<MF, VF, BF16P && L2, L2>, dim3(grid_for<false>(c->nchunks)), dim3(kThreads), s, descs_of(c, c->cur),
+                  c->d_chunk_tid, c->d_partial, k, c->chunk_log2, c->nchunks, c->gctl);
 }
 
 template <int MF, int VF, int SMODE, bool STATS>
-void launch_reduce(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
-  launch_k(c, k_reduce<MF, VF, SMODE, STATS>, dim3((unsigned)c->n), dim3(kReduceThreads), s,
-           descs_of(c, c->cur), c->d_partial, c->d_amax, c->d_old_scale, c->d_counters, c->chunk_log2,
-           c->d_flags, k.hist_len, k.hist_slot, c->gctl);
+int launch_reduce(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
+  return launch_k(c, k_reduce<MF, VF, SMODE, STATS>, dim3((unsigned)c->n), dim3(kReduceThreads), s,
+                  descs_of(c, c->cur), c->d_partial, c->d_amax, c->d_old_scale, c->d_counters, c->chunk_log2,
+                  c->d_flags, k.hist_len, k.hist_slot, c->gctl);
 }
 
 template <int MF, int VF, int SMODE>
-void launch_delayed_prepare(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
-  launch_k(c, k_delayed_prepare<MF, VF, SMODE>, dim3((unsigned)c->n), dim3(64), s, descs_of(c, 0), k,
-           c->d_old_scale);
+int launch_delayed_prepare(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
+  return launch_k(c, k_delayed_prepare<MF, VF, SMODE>, dim3((unsigned)c->n), dim3(64), s, descs_of(c, 0), k,
+                  c->d_old_scale);
 }
 
 template <int MF, int VF, int SMODE>
-void launch_delayed_reduce(fp8adam_ctx* c, const StepConsts& k, int part_log2, hipStream_t s) {
-  launch_k(c, k_delayed_reduce<MF, VF, SMODE>, dim3((unsigned)c->n), dim3(kReduceThreads), s,
-           descs_of(c, 0), c->d_part_amax, c->d_amax, k, c->chunk_log2, part_log2, c->gctl,
-           c->d_old_scale);
+int launch_delayed_reduce(fp8adam_ctx* c, const StepConsts& k, int part_log2, hipStream_t s) {
+  return launch_k(c, k_delayed_reduce<MF, VF, SMODE>, dim3((unsigned)c->n), dim3(kReduceThreads), s,
+                  descs_of(c, 0), c->d_part_amax, c->d_amax, k, c->chunk_log2, part_log2, c->gctl,
+                  c->d_old_scale);
 }
 
 template <int MF, int VF, bool BF16P, bool STATS, int SMODE, int MODE, bool L2, bool SR>
-void launch_update(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
+int launch_update(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
   const int64_t nwork = c->nchunks << (c->chunk_log2 - upd_part_log2<BF16P>());
-  launch_k(c, k_update<MF, VF, BF16P, STATS, SMODE, MODE, L2, SR>, dim3(grid_for<kXcdStreams>(nwork)), dim3(kThreads), s,
-           descs_of(c, c->cur), descs_of(c, MODE == kModeSpec ? 1 - c->cur : c->cur), c->d_chunk_tid, c->d_amax,
-           c->d_old_scale, k, c->d_counters, c->chunk_log2, c->d_part_amax, nwork, c->gctl);
+  return launch_k(c, k_update<MF, VF, BF16P, STATS, SMODE, MODE, L2, SR>, dim3(grid_for<kXcdStreams>(nwork)), dim3(kThreads), s,
+                  descs_of(c, c->cur), descs_of(c, MODE == kModeSpec ? 1 - c->cur : c->cur), c->d_chunk_tid, c->d_amax,
+                  c->d_old_scale, k, c->d_counters, c->chunk_log2, c->d_part_amax, nwork, c->gctl);
 }
 
 template <int MF, int VF, bool BF16P>
-void launch_spec_probe(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
-  launch_k(c, k_spec_probe<MF, VF, upd_part_log2<BF16P>()>,
-           dim3((unsigned)std::min<int64_t>(c->ncand_slots, kProbeGroups)), dim3(kThreads), s,
-           descs_of(c, c->cur), k, c->d_cand_count, c->d_cand_work, c->d_lb, c->gctl);
+int launch_spec_probe(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
+  return launch_k(c, k_spec_probe<MF, VF, upd_part_log2<BF16P>()>,
+                  dim3((unsigned)std::min<int64_t>(c->ncand_slots, kProbeGroups)), dim3(kThreads), s,
+                  descs_of(c, c->cur), k, c->d_cand_count, c->d_cand_work, c->d_lb, c->gctl);
 }
 
 template <int MF, int VF>
-void launch_spec_prepare(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
-  launch_k(c, k_spec_prepare<MF, VF>, dim3((unsigned)((c->n + 63) / 64)), dim3(64), s, descs_of(c, c->cur),
-           c->d_amax, k, c->gctl, c->d_old_scale, c->n, c->d_fix_count,
-           c->ncand_slots > 0 ? c->d_cand_n : nullptr, c->d_cand_len, c->d_lb, c->d_probed,
-           c->d_cand_count);
+int launch_spec_prepare(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
+  return launch_k(c, k_spec_prepare<MF, VF>, dim3((unsigned)((c->n + 63) / 64)), dim3(64), s, descs_of(c, c->cur),
+                  c->d_amax, k, c->gctl, c->d_old_scale, c->n, c->d_fix_count,
+                  c->ncand_slots > 0 ? c->d_cand_n : nullptr, c->d_cand_len, c->d_lb, c->d_probed,
+                  c->d_cand_count);
 }
 
 template <int MF, int VF>
-void launch_exact_prepare(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
-  launch_k(c, k_exact_prepare<MF, VF>, dim3((unsigned)c->n), dim3(kReduceThreads), s, descs_of(c, c->cur),
-           c->d_partial, c->chunk_log2, k, c->gctl, c->d_old_scale, c->d_fix_count, c->d_probed,
-           c->d_cand_count);
+int launch_exact_prepare(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
+  return launch_k(c, k_exact_prepare<MF, VF>, dim3((unsigned)c->n), dim3(kReduceThreads), s, descs_of(c, c->cur),
+                  c->d_partial, c->chunk_log2, k, c->gctl, c->d_old_scale, c->d_fix_count, c->d_probed,
+                  c->d_cand_count);
 }
 
 template <bool BF16P>
-void launch_part_fold(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
+int launch_part_fold(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
   const int split = c->chunk_log2 - upd_part_log2<BF16P>();
   const int64_t lanes = split > 1 ? (int64_t)1 << (split - 1) : 1;
-  launch_k(c, k_part_fold<upd_part_log2<BF16P>()>, dim3((unsigned)((c->nchunks * lanes + kThreads - 1) / kThreads)),
-           dim3(kThreads), s, c->d_part_amax, c->d_partial, c->chunk_log2, c->nchunks, k, c->gctl);
+  return launch_k(c, k_part_fold<upd_part_log2<BF16P>()>, dim3((unsigned)((c->nchunks * lanes + kThreads - 1) / kThreads)),
+                  dim3(kThreads), s, c->d_part_amax, c->d_partial, c->chunk_log2, c->nchunks, k, c->gctl);
 }
 
 template <int MF, int VF, bool STATS>
-void launch_spec_reduce(fp8adam_ctx* c, const StepConsts& k, int part_log2, hipStream_t s) {
-  launch_k(c, k_spec_reduce<MF, VF, STATS>, dim3((unsigned)c->n), dim3(kReduceThreads), s,
-           descs_of(c, c->cur), c->d_part_amax, c->ncand_slots > 0 ? c->d_partial : nullptr, c->d_amax, c->d_old_scale, c->d_flags, c->d_counters,
-           c->chunk_log2, part_log2, k, c->gctl, c->d_fix_count, c->d_fix_list, c->d_cand_n,
-           c->d_cand_len, c->d_cand_count, c->ncand_slots > 0 ? c->d_cand_work : nullptr);
+int launch_spec_reduce(fp8adam_ctx* c, const StepConsts& k, int part_log2, hipStream_t s) {
+  return launch_k(c, k_spec_reduce<MF, VF, STATS>, dim3((unsigned)c->n), dim3(kReduceThreads), s,
+                  descs_of(c, c->cur), c->d_part_amax, c->ncand_slots > 0 ? c->d_partial : nullptr, c->d_amax, c->d_old_scale, c->d_flags, c->d_counters,
+                  c->chunk_log2, part_log2, k, c->gctl, c->d_fix_count, c->d_fix_list, c->d_cand_n,
+                  c->d_cand_len, c->d_cand_count, c->ncand_slots > 0 ? c->d_cand_work : nullptr);
 }
 
 template <int MF, int VF, bool STATS, bool SR>
-void launch_fixup(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
+int launch_fixup(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
   // room for every chunk split down to the smallest piece, up to the fixed grid
   const int64_t groups = std::min<int64_t>((2 * c->nchunks) << (c->chunk_log2 - kFixPieceLog2Min), kFixGroups);
-  launch_k(c, k_fixup<MF, VF, STATS, SR>, dim3((unsigned)groups),
-           dim3(kThreads), s, descs_of(c, c->cur), descs_of(c, 1 - c->cur), c->d_chunk_tid, c->d_amax,
-           c->d_old_scale, k, c->d_counters, c->chunk_log2, c->d_fix_count, c->d_fix_list,
-           c->gctl);
+  return launch_k(c, k_fixup<MF, VF, STATS, SR>, dim3((unsigned)groups),
+                  dim3(kThreads), s, descs_of(c, c->cur), descs_of(c, 1 - c->cur), c->d_chunk_tid, c->d_amax,
+                  c->d_old_scale, k, c->d_counters, c->chunk_log2, c->d_fix_count, c->d_fix_list,
+                  c->gctl);
 }
 
 template <int MF, int VF, bool BF16P, bool STATS, int SMODE, bool L2, bool SR>
-void launch_block(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
-  launch_k(c, k_block<MF, VF, BF16P, STATS, SMODE, L2, SR>, dim3(grid_for<kXcdStreams>(c->nparts)), dim3(kThreads), s,
-           descs_of(c, 0), c->d_chunk_tid, k, c->d_counters, c->d_amax, c->chunk_log2, c->nparts, c->gctl);
+int launch_block(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
+  return launch_k(c, k_block<MF, VF, BF16P, STATS, SMODE, L2, SR>, dim3(grid_for<kXcdStreams>(c->nparts)), dim3(kThreads), s,
+                  descs_of(c, 0), c->d_chunk_tid, k, c->d_counters, c->d_amax, c->chunk_log2, c->nparts, c->gctl);
 }
 
 // Timing kinds: 0 amax pass, 1 update pass, 2 scale reduce, 3 block pass,
@@ -1816,13 +1816,13 @@ void launch_block(fp8adam_ctx* c, const StepConsts& k, hipStream_t s) {
   do {                                                 \
     int slot_;                                         \
     if (int r_ = timed_begin(c, (kind), s, &slot_)) return r_; \
-    call;                                              \
+    if (int r_ = (call)) return r_;                    \
     if (int r_ = timed_end(c, slot_, s)) return r_;    \
   } while (0)
 
-inline void launch_reset(fp8adam_ctx* c, int64_t namax, hipStream_t s) {
-  launch_k(c, k_reset, dim3(std::max<int64_t>(1, std::min<int64_t>(1024, (5 * (int64_t)c->n + 255) / 256))),
-           dim3(kThreads), s, c->d_counters, (int64_t)kStatsPerTensor * c->n, c->d_amax, namax);
+inline int launch_reset(fp8adam_ctx* c, int64_t namax, hipStream_t s) {
+  return launch_k(c, k_reset, dim3(std::max<int64_t>(1, std::min<int64_t>(1024, (5 * (int64_t)c->n + 255) / 256))),
+                  dim3(kThreads), s, c->d_counters, (int64_t)kStatsPerTensor * c->n, c->d_amax, namax);
 }
 
 template <int MF, int VF, bool BF16P, bool STATS, int SMODE, bool L2, bool SR>
@@ -1868,7 +1868,6 @@ int run_step_t(fp8adam_ctx* c, const StepConsts& k, int64_t t, hipStream_t s) {
     TIMED(2, (launch_reduce<MF, VF, SMODE, STATS>(c, k, s)));
     if (c->nchunks > 0) TIMED(1, (launch_update<MF, VF, BF16P, STATS, SMODE, kModeJit, L2, SR>(c, k, s)));
   }
-  HIP_TRY(hipGetLastError());
   return 0;
 }
 

@@ -12,7 +12,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PKG = os.path.join(ROOT, "precision_adam_optimizer_amd")
 
 
-@pytest.mark.parametrize("driver", ["list_launch_error_driver"])
+@pytest.mark.parametrize("driver", ["list_launch_error_driver", "step_launch_error_driver"])
 def test_launch_errors(tmp_path, driver):
     exe = str(tmp_path / driver)
     r = subprocess.run(["gcc", "-std=c11", "-O1", "-g", "-Wall", "-Werror", "-D__HIP_PLATFORM_AMD__",
