@@ -181,9 +181,10 @@ __device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv, bool 
 }
 
 // codes4 where the scale s is a power of two and the POW2 scale of the amax, so that
-// no value passes FMAX: the scaled converts divide by it as they round (the same
-// codes as encode4 of x / s over 8.6e9 pairs of values and scales, every scale
-// exponent and results down to zero among them), without clamps and products.
+// no value passes FMAX: the scaled converts divide by it as they round, without
+// clamps and products.  The codes are those of encode4 of x / s (tested at every
+// scale exponent: subnormal x, results down to zero, every tie of both formats and
+// the fp32 numbers beside it).
 template <int FMT>
 __device__ __forceinline__ uint32_t codes4_pow2(const float (&x)[4], float s, bool odd) {
   if (odd) return codes4<FMT>(x, 1.0f, true);  // such a block's scale is 1
