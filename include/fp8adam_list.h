@@ -57,7 +57,8 @@ void fp8adam_plan_destroy(fp8adam_plan *plan);
  * FP8ADAM_SCALE_BLOCK128 (given beta1 and beta2 that are fp32 numbers).
  * Not finite: a NaN or Inf gradient makes the moments and the weight what the formulas give (8-bit
  * moments: the block takes scale 1, an Inf saturates, a NaN becomes a NaN code); eps = 0 with
- * v' = 0 gives NaN.  With eps < 2^-38, a v'/(1-beta2^t) of 2^104 or more counts as Inf. */
+ * v' = 0 gives NaN.  With eps < 2^-38, a v'/(1-beta2^t) of 2^104 or more counts as Inf (2^80
+ * with an eps between 0 and 2^-114). */
 typedef struct {
     void *param;          /* weights, read and written */
     const void *grad;     /* gradients, read */

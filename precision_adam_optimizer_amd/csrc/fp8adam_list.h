@@ -235,7 +235,8 @@ struct AdamwDesc {
 // more that is less than half an ulp of their sum.  For a smaller eps the host
 // scales the denominator by denom_scale = 2^12 (eps and step_size by as much,
 // inv_bc2 by its square, which lifts every subnormal): the same bits otherwise, at
-// no cost here.
+// no cost here.  The hardware's reciprocal takes a subnormal denominator as 0 too:
+// the 2^24 for an eps below 2^-114 lift every eps that fp32 holds to 2^-125 or more.
 struct GroupConsts {
   float b1, omb1, b2, omb2;
   float lr_wd;      // lr * weight_decay
@@ -243,7 +244,9 @@ struct GroupConsts {
   float inv_bc2;    // 1 / (1 - beta2^t), times its square
   float eps;        // times denom_scale
 };
-inline double denom_scale(double eps) { return eps < 0x1p-38 ? 0x1p12 : 1.0; }
+inline double denom_scale(float eps) {
+  return eps >= 0x1p-38f ? 1.0 : eps >= 0x1p-114f || eps == 0.0f ? 0x1p12 : 0x1p24;
+}
 struct AdamwConsts {
   GroupConsts g[FP8ADAM_MAX_GROUPS];
 };

@@ -806,7 +806,7 @@ int check_groups(const fp8adam_plan* p, const fp8adam_adamw_hparams* h, int32_t 
     if (!isfinite(h[q].lr) || !isfinite(h[q].weight_decay))
       return fail(FP8ADAM_EINVAL, "lr and weight_decay must be finite");
     // what the kernels take of them in fp32 (1 / (1 - beta) bounds the bias corrections)
-    const double sc = denom_scale(h[q].eps);
+    const double sc = denom_scale((float)h[q].eps);
     if (!isfinite((float)(h[q].lr * sc / (1.0 - h[q].beta1))) || !isfinite((float)(h[q].lr * h[q].weight_decay)) ||
         !isfinite((float)h[q].eps) || !isfinite((float)(sc * sc / (1.0 - h[q].beta2))))
       return fail(FP8ADAM_EINVAL, "lr, lr * weight_decay, lr / (1 - beta1), 1 / (1 - beta2) and eps must be finite in fp32");
@@ -823,8 +823,8 @@ void group_consts(const fp8adam_adamw_hparams* h, int n_groups, int64_t t, Adamw
     c.b2 = (float)h[q].beta2;
     c.omb2 = (float)(1.0 - h[q].beta2);
     c.lr_wd = (float)(h[q].lr * h[q].weight_decay);
-    const double sc = denom_scale(h[q].eps);
-    c.eps = (float)(h[q].eps * sc);
+    const double sc = denom_scale((float)h[q].eps);
+    c.eps = (float)((float)h[q].eps * sc);
     c.step_size = t < 1 ? 0.0f : (float)(h[q].lr * sc / (1.0 - pow(h[q].beta1, (double)t)));
     c.inv_bc2 = t < 1 ? 0.0f : (float)(sc * sc / (1.0 - pow(h[q].beta2, (double)t)));
   }
@@ -1196,7 +1196,7 @@ int fp8adam_adamw_step_amp(fp8adam_plan* plan, const fp8adam_adamw_hparams* grou
     group_consts(groups, n_groups, 0, C);
     AmpArgs a{state, plan->d_ctl, *amp, n_groups, {}};
     for (int q = 0; q < n_groups; q++) {
-      const double sc = denom_scale(groups[q].eps);
+      const double sc = denom_scale((float)groups[q].eps);
       a.R.lr[q] = groups[q].lr * sc;
       a.R.beta1[q] = groups[q].beta1;
       a.R.beta2[q] = groups[q].beta2;
