@@ -13,7 +13,8 @@
  *                       (moments between 32 and 8 bits, weights for an FP8 forward pass).
  *
  * Each works through a plan: built once over a list, it holds the list's descriptors and the
- * workspace on the device.  A call enqueues its kernels on the given stream (0 = the null
+ * workspace on the device.  Building allocates and synchronizes the stream, which must not be
+ * under capture (EINVAL).  A call enqueues its kernels on the given stream (0 = the null
  * stream), allocates nothing, does not synchronize, and may be captured into a graph and
  * replayed.  Calls of one plan must not overlap (they share its workspace; neither may replays of
  * graphs that captured it); calls of different plans may, unless their tensors overlap.

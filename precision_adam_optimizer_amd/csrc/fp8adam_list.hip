@@ -741,8 +741,13 @@ struct Image {
   }
 };
 
-// The current device, which the stream has to belong to.
+// The current device, which the stream has to belong to.  Building allocates, copies and waits,
+// which a capture neither records nor survives: a stream that is being captured is refused first.
 int plan_device(fp8adam_plan* p, hipStream_t stream) {
+  hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+  HIP_TRY(hipStreamIsCapturing(stream, &capture));
+  if (capture != hipStreamCaptureStatusNone)
+    return fail(FP8ADAM_EINVAL, "the stream is being captured: build the plan before the capture");
   HIP_TRY(hipGetDevice(&p->device));
   hipDevice_t dev = -1;
   HIP_TRY(hipStreamGetDevice(stream, &dev));

@@ -190,11 +190,27 @@ def _blocks(numel: int) -> int:
     return -(-numel // BLOCK)
 
 
+def _capturing(device: torch.device) -> bool:
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
+_kept: list = []  # objects that were dropped while a graph was captured, with their plans
+
+
 class _Planned:
     """A plan on its device: calls go to the device's current stream."""
     _plan = None
 
+    def _check_capture(self, tensors) -> None:
+        """Before anything is allocated for a plan over these tensors."""
+        t = next((t for t in tensors if t.is_cuda), None)
+        if t is not None and _capturing(t.device):
+            raise RuntimeError("plans cannot be built while a graph is captured: build them before")
+
     def _build(self, device: torch.device, make) -> None:
+        while _kept:
+            _kept.pop().close()
         self.device = device
         self._index = device.index
         with torch.cuda.device(device):
@@ -213,7 +229,11 @@ class _Planned:
             _check(rc)
 
     def close(self) -> None:
+        """Waits for the device and frees the plan; no graph that captured one of its calls may be
+        replayed afterwards."""
         if self._plan:
+            if _capturing(self.device):
+                raise RuntimeError("a plan cannot be closed while a graph is captured")
             torch.cuda.synchronize(self.device)
             with torch.cuda.device(self.device):
                 fp8adam_plan_destroy(self._plan)
@@ -221,7 +241,10 @@ class _Planned:
 
     def __del__(self):
         try:
-            self.close()
+            if self._plan and _capturing(self.device):
+                _kept.append(self)  # waiting for the device would end the capture: the next plan frees this one
+            else:
+                self.close()
         except Exception:
             pass
 
@@ -260,6 +283,7 @@ class AdamW(_Planned):
             raise ValueError("copies, groups and state_bits need one entry per parameter")
         if any(b not in _MOMENTS for b in bits):
             raise ValueError("state_bits must be 32 or 8")
+        self._check_capture(params)
         self.n_groups = int(n_groups) if n_groups is not None else max(groups) + 1
         if not 1 <= self.n_groups <= MAX_GROUPS or any(not 0 <= q < self.n_groups for q in groups):
             raise ValueError(f"groups must lie in 0 .. n_groups - 1, with n_groups at most {MAX_GROUPS}")
@@ -367,6 +391,7 @@ class AdamW(_Planned):
             raise ValueError("state_bits must be 32 or 8")
         if granularity == "tensor" and (state_bits != 8 or any(b != 32 for b in self.state_bits)):
             raise ValueError("per-tensor scales are for 32-bit moments going to 8 bits")
+        self._check_capture(self.params)
         out = self.checkpoint()
         for k, fmt in enumerate(self.formats):
             idx = [i for i, b in enumerate(self.state_bits) if b != state_bits]
@@ -403,6 +428,7 @@ class GradClip(_Planned):
             _need(g.dtype in _DTYPES and (o is None or o.dtype in _DTYPES), i, "must be float32, bfloat16 or float16")
             _need(_dense(g) and (o is None or _dense(o)), i, "must be dense")
             _need(o is None or _same_order(g, o), i, "the output must have its gradient's size and order in memory")
+        self._check_capture(grads)
         dev = _one_gpu([t for x in (grads, outs) for t in x if t is not None])
         self.grads, self.outs = grads, outs
         args = [ClipTensorArg(_ptr(g), _ptr(o), g.numel(), _DTYPES[g.dtype], 0 if o is None else _DTYPES[o.dtype])
@@ -433,6 +459,7 @@ class Quantizer(_Planned):
         if not values:
             raise ValueError("need at least one tensor")
         n = len(values)
+        self._check_capture(values)
         fmts = [fmt] * n if isinstance(fmt, str) else list(fmt)
         block = _GRAN[granularity] == SCALE_BLOCK128
 

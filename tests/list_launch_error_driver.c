@@ -105,6 +105,30 @@ int main(void) {
     }
     stub_fail_malloc = 1;
     EXPECT(fp8adam_clip_plan(&p, &c, 1, NULL), FP8ADAM_ENOMEM, 0, hipSuccess);
+
+    /* a plan is not built on a stream that is being captured, and the capture sees nothing of it;
+     * the calls of a plan are captured */
+    fp8adam_plan *q = NULL;
+    EXPECT(fp8adam_clip_plan(&q, &c, 1, NULL), FP8ADAM_OK, 0, hipSuccess);
+    stub_capturing = 1;
+    stub_device_calls = 0;
+    fp8adam_adamw_tensor t;
+    memset(&t, 0, sizeof t);
+    t.param = (void *)(1ll << 40), t.grad = (void *)(2ll << 40), t.m = (void *)(3ll << 40), t.v = (void *)(4ll << 40);
+    t.numel = 10;
+    fp8adam_adamw_config acfg = {1, FP8ADAM_E4M3, FP8ADAM_E5M2, 0};
+    fp8adam_quant_tensor x = {(void *)(1ll << 40), (uint8_t *)(2ll << 40), (float *)(3ll << 40), 10, 0, 0};
+    fp8adam_quant_config qcfg = {FP8ADAM_SCALE_TENSOR, FP8ADAM_SCALE_POW2};
+    EXPECT(fp8adam_clip_plan(&p, &c, 1, NULL), FP8ADAM_EINVAL, 0, hipSuccess);
+    EXPECT(fp8adam_adamw_plan(&p, &t, 1, &acfg, NULL), FP8ADAM_EINVAL, 0, hipSuccess);
+    EXPECT(fp8adam_quant_plan(&p, &x, 1, &qcfg, NULL), FP8ADAM_EINVAL, 0, hipSuccess);
+    EXPECT(fp8adam_clip_grads(q, 1.0f, result, NULL), FP8ADAM_OK, 2, hipSuccess);
+    if (stub_device_calls) {
+        fprintf(stderr, "%d device calls during a capture\n", stub_device_calls);
+        failures++;
+    }
+    stub_capturing = 0;
+    fp8adam_plan_destroy(q);
     if (failures) return 1;
     printf("launch errors ok\n");
     return 0;

@@ -17,6 +17,8 @@ static int stub_launches = 0;       /* launches so far */
 static int stub_fail_launch = -1;   /* the launch that fails (counted from 0), or -1 */
 static int stub_fail_malloc = 0;    /* the next hipMalloc runs out of memory */
 static int stub_fail_memcpy = 0;    /* the next copy fails */
+static int stub_capturing = 0;      /* every stream is being captured */
+static int stub_device_calls = 0;   /* allocations, copies and waits so far: none belongs into a capture */
 
 static hipError_t stub_result(hipError_t e) {
     if (e != hipSuccess) stub_last = e;
@@ -31,14 +33,19 @@ hipError_t hipGetLastError(void) {
 
 hipError_t hipGetDevice(int *dev) { *dev = 0; return hipSuccess; }
 hipError_t hipStreamGetDevice(hipStream_t s, hipDevice_t *dev) { (void)s; *dev = 0; return hipSuccess; }
-hipError_t hipStreamSynchronize(hipStream_t s) { (void)s; return hipSuccess; }
+hipError_t hipStreamSynchronize(hipStream_t s) {
+    (void)s;
+    stub_device_calls++;
+    return hipSuccess;
+}
 hipError_t hipStreamIsCapturing(hipStream_t s, hipStreamCaptureStatus *c) {
     (void)s;
-    *c = hipStreamCaptureStatusNone;
+    *c = stub_capturing ? hipStreamCaptureStatusActive : hipStreamCaptureStatusNone;
     return hipSuccess;
 }
 
 hipError_t hipMalloc(void **p, size_t n) {
+    stub_device_calls++;
     if (stub_fail_malloc) {
         stub_fail_malloc = 0;
         return stub_result(hipErrorOutOfMemory);
@@ -51,6 +58,7 @@ hipError_t hipFree(void *p) { free(p); return hipSuccess; }
 hipError_t hipMemcpyAsync(void *d, const void *s, size_t n, hipMemcpyKind k, hipStream_t st) {
     (void)k;
     (void)st;
+    stub_device_calls++;
     if (stub_fail_memcpy) {
         stub_fail_memcpy = 0;
         return stub_result(hipErrorInvalidValue);
