@@ -19,6 +19,12 @@
  * replayed.  Calls of one plan must not overlap (they share its workspace; neither may replays of
  * graphs that captured it); calls of different plans may, unless their tensors overlap.
  *
+ * A replay takes what lies in device memory as it is then, and every argument from the host as it
+ * was at the capture: hyperparameters, max_norm, the scaler's factors, and fp8adam_adamw_step's
+ * `step`.  A replayed fp8adam_adamw_step therefore corrects its moments with the same t every
+ * time; training by replays takes fp8adam_adamw_step_amp, which counts t in device memory.  A
+ * new learning rate needs a new capture.
+ *
  * Conventions are fp8adam.h's: 0 or a negative FP8ADAM_E* code with fp8adam_last_error(); no
  * exception crosses the ABI; the plan belongs to the device that was current when it was built
  * and a stream of another device is refused.  Tensors are dense runs of `numel` elements at any
@@ -94,7 +100,9 @@ int fp8adam_adamw_step(fp8adam_plan *plan, const fp8adam_adamw_hparams *groups, 
 /* One step with loss scaling, skipping and clipping on the device, as fp8adam_step_amp: the norm
  * over every gradient of the list, the scaler's decision in *state (device memory, 8-byte aligned),
  * then the step with every gradient multiplied by state's grad_factor and t = state's step, or
- * nothing if a gradient was not finite.  With a scale of 1 it is a step with clipping alone. */
+ * nothing if a gradient was not finite.  With a scale of 1 and a growth_interval out of reach
+ * (INT32_MAX) it is a step with clipping alone, for as long as no step is skipped: a skipped one
+ * lowers the scale, which the program then sets back. */
 int fp8adam_adamw_step_amp(fp8adam_plan *plan, const fp8adam_adamw_hparams *groups, int32_t n_groups,
                            const fp8adam_amp_config *amp, fp8adam_amp_state *state, hipStream_t stream);
 

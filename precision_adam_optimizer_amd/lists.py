@@ -268,6 +268,11 @@ class AdamW(_Planned):
     or (m, v, m_scale, v_scale) with None where moments have 32 bits); fresh ones
     otherwise.  The tensors must stay alive with the same storage while this
     object exists, and none that a step writes may overlap another.
+
+    Steps may be captured into a graph (of this class and of ``GradClip`` and
+    ``Quantizer``; the object must outlive it).  A replay takes what is not a
+    tensor as it was at the capture: the hyperparameters, ``max_norm`` and ``step``.
+    Training by replays therefore takes ``step_amp``, which counts t on the device.
     """
 
     def __init__(self, params, grads, *, state_bits=32, copies=None, groups=None, n_groups=None, m_format="e4m3",
@@ -365,7 +370,8 @@ class AdamW(_Planned):
                  growth_interval: int = 2000) -> None:
         """A step on gradients of (loss * scale), as ``FP8AdamW.step_amp``: unscale, skip on
         Inf/NaN, clip the global norm to max_norm (if > 0), all on the device.  t is the
-        state's count of taken steps (``amp_state()`` starts it at 0)."""
+        state's count of taken steps (``amp_state()`` starts it at 0).  For gradients that are not
+        scaled: a state of scale 1 and growth_interval=2**31 - 1; a skipped step still lowers the scale."""
         if amp_state.dtype != torch.uint8 or amp_state.numel() != AMP_STATE_DTYPE.itemsize:
             raise ValueError("amp_state must be the 32-byte tensor from amp_state()")
         if amp_state.device != self.device or not amp_state.is_contiguous():

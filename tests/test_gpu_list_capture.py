@@ -5,6 +5,7 @@ import torch
 
 import precision_adam_optimizer_amd as pk
 from precision_adam_optimizer_amd import lists
+from tests.test_gpu_list import HP, Case, gen, optimizer
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +48,71 @@ def test_plans_and_a_capture():
     again.close()
     clip.close()
     bits.close()
+
+
+def make(seed):
+    g = gen(seed)
+    cases = [Case(n, g, bits=bits, gscale=0.1) for n in (1500, 129) for bits in (32, 8)]
+    return cases, optimizer(cases)
+
+
+def state(cases):
+    return [t.clone() for c in cases for t in (c.p, c.m, c.v, c.ms, c.vs) if t is not None]
+
+
+def new_gradients(cases, others, k):
+    for i, (x, y) in enumerate(zip(cases, others)):
+        x.g.copy_(torch.randn(x.n, generator=gen(100 * k + i), device="cuda"))
+        y.g.copy_(x.g)
+
+
+def test_a_replayed_step_takes_its_arguments_from_the_capture():
+    """Every replay is the step with the capture's t and rates on the gradients of now."""
+    (a, oa), (b, ob) = make(30), make(30)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        oa.step(step=2, **HP)
+    oa._set(0.0, 0.0, 0.0, 1.0, 0.0)  # what the host holds now is nothing to the graph
+    for k in range(3):
+        new_gradients(a, b, k)
+        graph.replay()
+        torch.cuda.synchronize()
+        ob.step(step=2, **HP)
+        assert all(torch.equal(x, y) for x, y in zip(state(a), state(b))), k
+    new_gradients(a, b, 3)
+    graph.replay()
+    ob.step(step=3, **HP)
+    assert not all(torch.equal(x, y) for x, y in zip(state(a), state(b)))  # not the next step
+    oa.close()
+    ob.close()
+
+
+def test_training_by_replays_of_the_scaled_step():
+    """A scale of 1 that never grows: replays are the plain steps 1, 2, 3, ... (their factor is 1, and t
+    is the device's), the eager calls among them too."""
+    (a, oa), (b, ob) = make(31), make(31)
+    amp = pk.amp_state(1.0)
+    kw = dict(growth_interval=2 ** 31 - 1, **HP)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        oa.step_amp(amp, **kw)
+    for t in range(1, 7):
+        new_gradients(a, b, t)
+        if t == 4:
+            oa.step_amp(amp, **kw)
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        st = pk.read_amp_state(amp)
+        assert (st["step"], st["scale"], st["grad_factor"]) == (t, 1.0, 1.0)
+        ob.step(step=t, **HP)
+        for x, y in zip(a, b):
+            # moments do not see t; the weights' bias corrections come from the device's pow and the host's,
+            # each within an ulp of double before it is rounded to fp32: one step of fp32 apart at most, which
+            # moves the update by 2u + u and its roundings by as much as they move the plain step's (12u of
+            # test_gpu_list.py, on both sides)
+            assert torch.equal(x.m, y.m) and torch.equal(x.v, y.v)
+            assert bool(((x.p - y.p).abs() <= 2.0 ** -24 * (27 * 10 * HP["lr"] + 2 * y.p.abs())).all())
+            x.p.copy_(y.p)
+    oa.close()
+    ob.close()
