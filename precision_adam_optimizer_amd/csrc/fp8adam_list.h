@@ -382,7 +382,7 @@ __device__ __forceinline__ void adamw_whole(const AdamwDesc& d, const GroupConst
 // their own rates.
 // 842M bf16 weights with bf16 gradients and 8-bit moments (10.1 bytes): 1.35 ms,
 // 6.3 TB/s, 95% of that bound.  The smallest lists are bound by the launch: 65
-// tensors of 4096 take 3 us on the device, 5.7 us with the call.  Packed fp32
+// tensors of 4096 take 3 us on the device, 5.5 us with the call.  Packed fp32
 // tensors of odd sizes cost no more (every fp32 stream starts on a dword): 7M
 // weights in 48 of them 35 us, 5.7 TB/s.
 template <int PD, int CD, int GD, bool S8, int MF, int VF>

@@ -240,8 +240,10 @@ __global__ __launch_bounds__(kThreads) void k_list_ctl(const double* __restrict_
 // arrives last (by a ticket of the plan's workspace, zero before and after) sums the
 // partials, in their order, and decides.  Its ticket's acquire sees the partials,
 // each stored before its work-group's release.  A release costs more the more
-// work-groups make one (100 us of 2048), a launch of its own about 5: a scaled step
-// over 1 to 64 tensors of 4000 takes 10.8 us with the ticket, 13.4 without.
+// work-groups make one (100 us of 2048).  Among other calls, where the host's
+// launches count, a scaled step over 1 to 64 tensors of 4000 takes 9.7 to 11.4 us
+// with the ticket and 12.1 to 12.4 without; replayed from a graph the two are within
+// 0.4 us of each other (8.1 to 10.5), the ticket ahead on one chunk and behind on 64.
 constexpr int kTicketGroups = 64;
 
 __global__ __launch_bounds__(kThreads) void k_list_sumsq_ctl(const GradDesc* __restrict__ descs,
