@@ -32,7 +32,10 @@
  * Conventions for every entry point:
  *   - Return 0 on success or a negative FP8ADAM_E* code; fp8adam_last_error()
  *     then gives a message (thread-local, valid until the next call on that
- *     thread).  Nothing aborts and no C++ exception crosses the ABI.
+ *     thread).  Nothing aborts and no C++ exception crosses the ABI.  A failed
+ *     HIP call is reported once, with EHIP or ENOMEM: it does not stay behind as
+ *     the thread's last HIP error, and one that the thread held before is neither
+ *     reported nor, by a call that succeeds, taken.
  *   - Pointers named "device" are HIP device memory of the current device;
  *     pointers named "host" are ordinary host memory.
  *   - Work is enqueued on the given stream (0 = the null stream) and runs

@@ -79,6 +79,27 @@ static void steps(const char *what, int64_t t) {
     hp.step = t;
     check(what, step);
     check(what, step_amp);
+    /* timed: a launch that fails is not among the timed ones */
+    int last = -1;
+    for (int k = 0; last != FP8ADAM_OK; k++) {
+        double ms[32];
+        int32_t count[32], sum = 0;
+        if (fp8adam_set_timing(c, 1) != FP8ADAM_OK) failures++;
+        stub_launches = 0;
+        stub_last = hipSuccess;
+        stub_fail_launch = k;
+        last = step_amp();
+        if (last != FP8ADAM_OK) expect(what, last, FP8ADAM_EHIP, k, hipSuccess, fp8adam_last_error());
+        const int launched = last == FP8ADAM_OK ? stub_launches : k;
+        if (fp8adam_kernel_times(c, ms, count, 32) != FP8ADAM_OK) failures++;
+        for (int i = 0; i < 32; i++) sum += count[i];
+        if (sum != launched) {
+            fprintf(stderr, "%s: %d kernels timed of %d\n", what, sum, launched);
+            failures++;
+        }
+    }
+    stub_fail_launch = -1;
+    stub_launches = 0;
     fp8adam_destroy(c);
     ctx = NULL;
 }

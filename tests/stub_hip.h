@@ -79,6 +79,15 @@ hipError_t hipGetSymbolAddress(void **p, const void *sym) {
     return hipSuccess;
 }
 
+hipError_t hipEventCreate(hipEvent_t *e) { *e = (hipEvent_t)malloc(1); return hipSuccess; }
+hipError_t hipEventDestroy(hipEvent_t e) { free(e); return hipSuccess; }
+hipError_t hipEventSynchronize(hipEvent_t e) { (void)e; return hipSuccess; }
+hipError_t hipEventElapsedTime(float *ms, hipEvent_t a, hipEvent_t b) {
+    (void)a, (void)b;
+    *ms = 1.0f;
+    return hipSuccess;
+}
+
 static hipError_t stub_launch(void) {
     if (stub_launches == stub_fail_launch) return stub_result(hipErrorLaunchFailure);
     stub_launches++;
