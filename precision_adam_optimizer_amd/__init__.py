@@ -5,7 +5,9 @@ the functions below carry the C names and only marshal arguments; every step
 of the optimizer runs in the library's HIP kernels.  PyTorch supplies device
 memory and the stream.  There is no fallback: if the library is missing,
 ``load()`` raises.  The list operators (``AdamW``, ``GradClip``, ``Quantizer``;
-C ABI in ``include/fp8adam_list.h``) are in ``lists.py`` and reached from here.
+C ABI in ``include/fp8adam_list.h``) are in ``lists.py``, the layer operators
+(``linear8``, ``gated8`` and their backward passes on ``Packed8`` matrices; C ABI in
+``include/fp8adam_layer.h``) in ``layers.py``, both reached from here.
 """
 from __future__ import annotations
 
@@ -503,3 +505,15 @@ from .lists import (  # noqa: E402
     fp8adam_plan_destroy, fp8adam_quant_plan, fp8adam_quantize)
 
 EXPORTS += LIST_EXPORTS
+
+# ------------------------------------------------------------ layer operators
+
+from .layers import (  # noqa: E402
+    ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, LAYER_EXPORTS, LAYER_MAX_COLS, LAYER_MAX_LD, SCALES_E8M0, SCALES_F32,
+    ActBackward8Arg, Gated8, Grad8Arg, Linear8, Matrix8Arg, MatrixArg, Packed8, Product8Arg, fp8adam_gated8,
+    fp8adam_gated8_backward, fp8adam_input_grad8, fp8adam_input_grad8_workspace, fp8adam_linear8,
+    fp8adam_linear8_backward, fp8adam_linear8_backward_workspace, fp8adam_pack8, fp8adam_unpack8,
+    fp8adam_weight_grad8, fp8adam_weight_grad8_workspace, gated8, gated8_backward, input_grad8, linear8,
+    linear8_backward, pack8, unpack8, weight_grad8)
+
+EXPORTS += LAYER_EXPORTS

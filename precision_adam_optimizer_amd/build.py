@@ -3,7 +3,8 @@
 The step kernels are instantiated in one translation unit per (m, v) format
 pair (``csrc/fp8adam_step_*.hip``) and the C ABI is in ``csrc/fp8adam.hip``,
 that of the list operators in ``csrc/fp8adam_list.hip`` (their AdamW kernels in
-``csrc/fp8adam_list_adamw*.hip``); the units compile in parallel, then link into one shared library.
+``csrc/fp8adam_list_adamw*.hip``), that of the layer operators in ``csrc/fp8adam_layer.hip`` (their products
+in ``csrc/fp8adam_layer_*.hip``); the units compile in parallel, then link into one shared library.
 """
 from __future__ import annotations
 
@@ -17,10 +18,9 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-UNITS = [os.path.join(CSRC, "fp8adam.hip"), os.path.join(CSRC, "fp8adam_list.hip")] + sorted(
-    glob.glob(os.path.join(CSRC, "fp8adam_step_*.hip")) + glob.glob(os.path.join(CSRC, "fp8adam_list_adamw*.hip")))
-DEPS = UNITS + [os.path.join(CSRC, h) for h in ("fp8_codec.h", "fp8adam_engine.h", "fp8adam_list.h")] + [
-    os.path.join(ROOT, "include", h) for h in ("fp8adam.h", "fp8adam_list.h")]
+UNITS = [os.path.join(CSRC, f"fp8adam{x}.hip") for x in ("", "_list", "_layer")] + sorted(
+    x for pattern in ("step_*", "list_adamw*", "layer_*") for x in glob.glob(os.path.join(CSRC, f"fp8adam_{pattern}.hip")))
+DEPS = UNITS + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
 LIB = os.path.join(PKG, "libfp8adam.so")
 ARCH = "gfx950"
 

@@ -1,0 +1,9 @@
+// fp8adam_layer_product_e4m3_e4m3.hip -- instantiates the forward products of inputs in E4M3 and weights in
+// E4M3 (one translation unit per format pair, so the library builds in parallel).
+#include "fp8adam_layer_product.h"
+
+namespace fp8adam_layer {
+
+template int launch_product<0, 0>(const ProductArgs&, bool, hipStream_t);
+
+}  // namespace fp8adam_layer

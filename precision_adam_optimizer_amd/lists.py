@@ -486,6 +486,7 @@ class Quantizer(_Planned):
             _check_flat(s, i, "scales", torch.float32, count(x), True)
         dev = _one_gpu(values + codes + scales)
         self.values, self.codes, self.scales = values, codes, scales
+        self.formats, self.granularity, self.scale_mode = fmts, granularity, scale_mode
         args = [QuantTensorArg(_ptr(x), _ptr(c), _ptr(s), x.numel(), _DTYPES[x.dtype], _FORMATS[f])
                 for x, c, s, f in zip(values, codes, scales, fmts)]
         cfg = QuantConfigArg(_GRAN[granularity], _SMODE[scale_mode])
