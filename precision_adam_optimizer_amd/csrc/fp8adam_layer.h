@@ -12,7 +12,6 @@ using namespace fp8adam;
 using namespace fp8adam_engine;
 using fp8adam_list::codes4_pow2;
 using fp8adam_list::dtype_bytes;
-using fp8adam_list::half_wave_max;
 using fp8adam_list::ld_elem;
 using fp8adam_list::nonfinite_amax;
 using fp8adam_list::pack4;
@@ -23,6 +22,7 @@ using fp8adam_list::vu2_any;
 using fp8adam_list::vu4_any;
 
 typedef float vf4_t __attribute__((ext_vector_type(4)));
+typedef float vf16_t __attribute__((ext_vector_type(16)));
 
 // ------------------------------------------------------------------- typed rows
 
@@ -53,6 +53,37 @@ __device__ __forceinline__ void st4(void* base, int64_t i, int64_t n, const floa
   }
 }
 
+typedef vu4 __attribute__((aligned(2))) vu4_any2;
+
+template <int DT>
+__device__ __forceinline__ void ld8(const void* base, int64_t i, int64_t n, float (&x)[8]) {
+  float a[4], b[4];
+  if (DT != FP8ADAM_F32 && n >= 8) {
+    constexpr int D = DT == FP8ADAM_F32 ? FP8ADAM_BF16 : DT;
+    const vu4 w = ld_global<vu4_any2>(static_cast<const char*>(base) + 2 * i);
+    unpack4<D>(Raw4<D>{vu2{w.x, w.y}}, a);
+    unpack4<D>(Raw4<D>{vu2{w.z, w.w}}, b);
+  } else {
+    ld4<DT>(base, i, n, a);
+    ld4<DT>(base, i + 4, n - 4, b);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; j++) x[j] = a[j], x[4 + j] = b[j];
+}
+
+template <int DT>
+__device__ __forceinline__ void st8(void* base, int64_t i, int64_t n, const float (&x)[8]) {
+  const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
+  if (DT != FP8ADAM_F32 && n >= 8) {
+    constexpr int D = DT == FP8ADAM_F32 ? FP8ADAM_BF16 : DT;
+    const vu2 p = pack4<D>(a).x, q = pack4<D>(b).x;
+    st_global<vu4_any2>(static_cast<char*>(base) + 2 * i, vu4{p.x, p.y, q.x, q.y});
+  } else {
+    st4<DT>(base, i, n, a);
+    st4<DT>(base, i + 4, n - 4, b);
+  }
+}
+
 // The same with the type known at run time (the same in every lane).
 __device__ __forceinline__ void ld4(int dt, const void* base, int64_t i, int64_t n, float (&x)[4]) {
   if (dt == FP8ADAM_F32) ld4<FP8ADAM_F32>(base, i, n, x);
@@ -63,6 +94,17 @@ __device__ __forceinline__ void st4(int dt, void* base, int64_t i, int64_t n, co
   if (dt == FP8ADAM_F32) st4<FP8ADAM_F32>(base, i, n, x);
   else if (dt == FP8ADAM_BF16) st4<FP8ADAM_BF16>(base, i, n, x);
   else st4<FP8ADAM_F16>(base, i, n, x);
+}
+
+__device__ __forceinline__ void ld8(int dt, const void* base, int64_t i, int64_t n, float (&x)[8]) {
+  if (dt == FP8ADAM_F32) ld8<FP8ADAM_F32>(base, i, n, x);
+  else if (dt == FP8ADAM_BF16) ld8<FP8ADAM_BF16>(base, i, n, x);
+  else ld8<FP8ADAM_F16>(base, i, n, x);
+}
+__device__ __forceinline__ void st8(int dt, void* base, int64_t i, int64_t n, const float (&x)[8]) {
+  if (dt == FP8ADAM_F32) st8<FP8ADAM_F32>(base, i, n, x);
+  else if (dt == FP8ADAM_BF16) st8<FP8ADAM_BF16>(base, i, n, x);
+  else st8<FP8ADAM_F16>(base, i, n, x);
 }
 
 // ------------------------------------------------------------------ activations
@@ -124,13 +166,17 @@ __device__ __forceinline__ void act_slope(float z, float& a, float& da) {
 }
 
 // With the activation known at run time (the same in every lane).
-__device__ __forceinline__ void act4(int which, float (&z)[4]) {
+template <int N, int M>
+__device__ __forceinline__ void act_all(int which, float (&z)[N][M]) {
+  auto all = [&](auto f) {
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    if (which == FP8ADAM_ACT_RELU) z[j] = act<FP8ADAM_ACT_RELU>(z[j]);
-    else if (which == FP8ADAM_ACT_SILU) z[j] = act<FP8ADAM_ACT_SILU>(z[j]);
-    else if (which == FP8ADAM_ACT_GELU) z[j] = act<FP8ADAM_ACT_GELU>(z[j]);
-  }
+    for (int i = 0; i < N; i++)
+#pragma unroll
+      for (int j = 0; j < M; j++) z[i][j] = f(z[i][j]);
+  };
+  if (which == FP8ADAM_ACT_RELU) all(act<FP8ADAM_ACT_RELU>);
+  else if (which == FP8ADAM_ACT_SILU) all(act<FP8ADAM_ACT_SILU>);
+  else if (which == FP8ADAM_ACT_GELU) all(act<FP8ADAM_ACT_GELU>);
 }
 
 // -------------------------------------------------------- blocks of 128 in 8 bits
@@ -143,23 +189,66 @@ struct Out8 {
   int32_t format;
 };
 
-// The block that 32 lanes hold, four consecutive values each (zeros behind the row's end, whose
-// codes are zeros): its codes and its scale to column 128 * block of a row.  `lane` is the lane
-// in the half-wave; all 32 come here.
-template <int FMT>
-__device__ __forceinline__ void put_block(const Out8& o, int64_t row, int64_t block, int lane, const float (&x)[4]) {
-  uint32_t am = 0;
-#pragma unroll
-  for (int j = 0; j < 4; j++) am = max(am, abs_bits(x[j]));
-  am = half_wave_max(am);
-  float s, inv;
-  choose_scale<FMT, 0>(am, s, inv);
-  st_global<uint32_t>(o.codes + row * o.ld + 128 * block + 4 * lane, codes4_pow2<FMT>(x, s, nonfinite_amax(am)));
-  if (lane == 0) st_global<uint8_t>(o.scales + row * o.ld_scale + block, (uint8_t)(__float_as_uint(s) >> 23));
+// The largest of 16 lanes in each of them: maxima with fused DPP operands.
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));   // quad_perm [1,0,3,2]
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));   // quad_perm [2,3,0,1]
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));  // row_half_mirror
+  return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, true));  // row_mirror
 }
-__device__ __forceinline__ void put_block(const Out8& o, int64_t row, int64_t block, int lane, const float (&x)[4]) {
-  if (o.format == FP8ADAM_E4M3) put_block<0>(o, row, block, lane, x);
-  else put_block<1>(o, row, block, lane, x);
+
+// choose_scale's POW2 scale as its exponent's byte, without branches: a subnormal amax comes out at the
+// lower limit by itself.
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  const int k = (int)(amax >> 23) + (1 - Format<FMT>::kMaxExp) + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  const int byte = min(max(k, 1), 253);
+  return amax - 1u < 0x7F7FFFFFu ? (uint32_t)byte : 127u;  // zero, Inf and NaN: 1
+}
+
+// N blocks that 16 lanes hold, eight consecutive values each (zeros behind the row's end, whose
+// codes are zeros): their codes and scales to column 128 * block[i] of row[i] where `there`.  `lane` is the
+// lane among the 16, all of which come here and agree on the rest.
+template <int FMT, int N>
+__device__ __forceinline__ void put_blocks_as(const Out8& o, const int64_t (&row)[N], const int64_t (&block)[N], const bool (&there)[N],
+                                              int lane, const float (&x)[N][8]) {
+  uint32_t am[N], byte[N];
+  vu2 codes[N];
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    am[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j++) am[i] = max(am[i], abs_bits(x[i][j]));
+  }
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    am[i] = row_max(am[i]);
+    byte[i] = scale_byte<FMT>(am[i]);
+    const float s = __uint_as_float(byte[i] << 23);
+    const float lo[4] = {x[i][0], x[i][1], x[i][2], x[i][3]}, hi[4] = {x[i][4], x[i][5], x[i][6], x[i][7]};
+    codes[i] = vu2{codes4_pow2<FMT>(lo, s, false), codes4_pow2<FMT>(hi, s, false)};
+    any = any || nonfinite_amax(am[i]);
+  }
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(any) != 0, 0)) {  // uniform: one test for the wave
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const float lo[4] = {x[i][0], x[i][1], x[i][2], x[i][3]}, hi[4] = {x[i][4], x[i][5], x[i][6], x[i][7]};
+      if (nonfinite_amax(am[i])) codes[i] = vu2{codes4_pow2<FMT>(lo, 1.0f, true), codes4_pow2<FMT>(hi, 1.0f, true)};
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; i++)
+    if (there[i]) st_global<vu2>(o.codes + row[i] * o.ld + 128 * block[i] + 8 * lane, codes[i]);
+#pragma unroll
+  for (int i = 0; i < N; i++)
+    if (there[i] && lane == 0) st_global<uint8_t>(o.scales + row[i] * o.ld_scale + block[i], (uint8_t)byte[i]);
+}
+template <int N>
+__device__ __forceinline__ void put_blocks(const Out8& o, const int64_t (&row)[N], const int64_t (&block)[N], const bool (&there)[N],
+                                           int lane, const float (&x)[N][8]) {
+  if (o.format == FP8ADAM_E4M3) put_blocks_as<0, N>(o, row, block, there, lane, x);
+  else put_blocks_as<1, N>(o, row, block, there, lane, x);
 }
 
 // The scale of block `block` of row `row`.
@@ -170,16 +259,57 @@ __device__ __forceinline__ float scale_at(const void* scales, int64_t i, bool f3
 
 // ------------------------------------------------- direct loads into shared memory
 
-typedef __attribute__((address_space(3))) void* LdsPtr;
+// A buffer resource as four scalars, for the loads below.
+__device__ __forceinline__ vu4 rsrc4(const void* base, int64_t bytes) {
+  const uint64_t p = (uint64_t)(uintptr_t)base;
+  return vu4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p), (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32)),
+             (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), (uint32_t)kRawBufferWord3};
+}
 
 // 16 bytes per lane, to dst + 16 * lane (dst the same in every lane of the wave); lanes whose
-// offset lies outside the resource write zeros.
-__device__ __forceinline__ void load_lds(Rsrc r, uint8_t* dst, uint32_t voffset, uint32_t soffset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)dst, 16, voffset, soffset, 0, 0);
+// offset lies outside the resource write zeros.  In assembly (it has no register output), because the
+// compiler waits for every such load it knows of before it reads shared memory; the kernels
+// count them themselves (stage_barrier).  A write of m0 needs one wait state before the load.
+__device__ __forceinline__ void load_lds(const vu4& r, const uint8_t* dst, uint32_t voffset, uint32_t soffset) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)dst;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane((int)at)), "v"(voffset), "s"(r), "s"(soffset)
+               : "memory", "m0");
+}
+
+// The same of one scale per lane, to dst + 4 * lane: a 32-bit number, or a byte widened to 32 bits.
+__device__ __forceinline__ void load_lds_scalars(const vu4& r, const uint8_t* dst, uint32_t voffset, bool dwords) {
+  const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)dst);
+  if (dwords)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "s"(at), "v"(voffset), "s"(r) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" : : "s"(at), "v"(voffset), "s"(r) : "memory", "m0");
 }
 
 // The loads above are counted as vector memory loads: a barrier alone does not wait for them.
 __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
+
+// Between the stages of a pipeline in shared memory: at most N of this wave's loads are still on their way,
+// its reads and writes of shared memory are done, and so are those of the other waves.  (A
+// __syncthreads() would wait for every load.)
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+  static_assert(N < 64, "the counter's six bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (N >> 4) << 14);  // vmcnt(N), lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// A barrier that waits for nothing else, and that nothing is moved across.
+__device__ __forceinline__ void bare_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
 
 // ----------------------------------------------------------------- forward product
 

@@ -21,27 +21,27 @@ namespace {
 
 // ------------------------------------------------------------ to 8 bits and back
 
-// Blocks per half-wave, whose loads go out together.
+// Blocks per 16 lanes, whose loads go out together.
 constexpr int kPackUnroll = 4;
-constexpr int kPackBlocks = kThreads / 32 * kPackUnroll;  // of a work-group
+constexpr int kPackBlocks = kThreads / 16 * kPackUnroll;  // of a work-group
 
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_pack(const void* x, int64_t ld, Out8 o, int64_t rows, int cols, int64_t nb) {
-  const int lane = threadIdx.x & 31;
-  const int64_t first = (int64_t)blockIdx.x * kPackBlocks + (threadIdx.x >> 5), total = rows * nb;
-  float v[kPackUnroll][4];
+  const int lane = threadIdx.x & 15;
+  const int64_t first = (int64_t)blockIdx.x * kPackBlocks + (threadIdx.x >> 4), total = rows * nb;
+  float v[kPackUnroll][8];
   int64_t row[kPackUnroll], blk[kPackUnroll];
+  bool there[kPackUnroll];
 #pragma unroll
   for (int u = 0; u < kPackUnroll; u++) {
-    const int64_t i = first + u * (kThreads / 32);
+    const int64_t i = first + u * (kThreads / 16);
+    there[u] = i < total;
     row[u] = total >> 32 ? i / nb : (uint32_t)i / (uint32_t)nb;
     blk[u] = i - row[u] * nb;
-    const int64_t c = 128 * blk[u] + 4 * lane;
-    ld4<DT>(x, row[u] * ld + c, i < total ? cols - c : 0, v[u]);
+    const int64_t c = 128 * blk[u] + 8 * lane;
+    ld8<DT>(x, row[u] * ld + c, there[u] ? cols - c : 0, v[u]);
   }
-#pragma unroll
-  for (int u = 0; u < kPackUnroll; u++)
-    if (first + u * (kThreads / 32) < total) put_block(o, row[u], blk[u], lane, v[u]);
+  put_blocks(o, row, blk, there, lane, v);
 }
 
 // Eight codes times their scale.
@@ -59,36 +59,6 @@ __device__ __forceinline__ void decode8(int format, const vu2& c, float s, float
     }
     x[2 * q] = v[0];
     x[2 * q + 1] = v[1];
-  }
-}
-
-template <int DT>
-__device__ __forceinline__ void ld8(const void* base, int64_t i, int64_t n, float (&x)[8]) {
-  float a[4], b[4];
-  if (DT != FP8ADAM_F32 && n >= 8) {
-    typedef vu4 __attribute__((aligned(2))) vu4_any2;
-    const vu4 w = ld_global<vu4_any2>(static_cast<const char*>(base) + 2 * i);
-    unpack4<DT == FP8ADAM_F32 ? FP8ADAM_BF16 : DT>({vu2{w.x, w.y}}, a);
-    unpack4<DT == FP8ADAM_F32 ? FP8ADAM_BF16 : DT>({vu2{w.z, w.w}}, b);
-  } else {
-    ld4<DT>(base, i, n, a);
-    ld4<DT>(base, i + 4, n - 4, b);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; j++) x[j] = a[j], x[4 + j] = b[j];
-}
-
-template <int DT>
-__device__ __forceinline__ void st8(void* base, int64_t i, int64_t n, const float (&x)[8]) {
-  const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
-  if (DT != FP8ADAM_F32 && n >= 8) {
-    typedef vu4 __attribute__((aligned(2))) vu4_any2;
-    constexpr int D = DT == FP8ADAM_F32 ? FP8ADAM_BF16 : DT;
-    const auto p = pack4<D>(a).x, q = pack4<D>(b).x;
-    st_global<vu4_any2>(static_cast<char*>(base) + 2 * i, vu4{p.x, p.y, q.x, q.y});
-  } else {
-    st4<DT>(base, i, n, a);
-    st4<DT>(base, i + 4, n - 4, b);
   }
 }
 
@@ -639,7 +609,7 @@ auto guarded(const char* what, F&& body) -> decltype(body()) {
 }  // namespace
 
 GradPlan plan_grad(int64_t m, int64_t k, int64_t r, int npairs) {
-  const int64_t steps = (r + 63) / 64 * npairs;
+  const int64_t steps = (r + 63) / 64 * npairs;  // of two stages
   auto tiles = [&](int64_t t) { return std::max<int64_t>(1, (m + t - 1) / t * ((k + t - 1) / t)); };
   auto parts = [&](int64_t t, int64_t slots) { return std::max<int64_t>(1, std::min<int64_t>(slots / tiles(t), steps / 8)); };
   GradPlan p{0, (int)parts(256, 256), 0};
