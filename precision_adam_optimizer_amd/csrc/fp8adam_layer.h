@@ -344,7 +344,11 @@ constexpr int kFewTokens = 64, kFewPackTokens = 16;
 inline bool few_tokens(const ProductArgs& a) {
   return a.tokens <= kFewTokens && !a.keep[0].codes && !a.keep[1].codes && !a.y8.codes;
 }
-inline bool packs_itself(const ProductArgs& a) { return few_tokens(a) && a.tokens <= kFewPackTokens; }
+inline bool packs_itself(const ProductArgs& a, const fp8adam_matrix& x) {  // rows of whole dwords
+  const int64_t e = dtype_bytes(x.dtype);
+  return few_tokens(a) && a.tokens <= kFewPackTokens && (uintptr_t)x.data % 4 == 0 && a.cols * e % 4 == 0 &&
+         (a.tokens == 1 || x.ld * e % 4 == 0);
+}
 
 template <int XF, int WF>
 int launch_product(const ProductArgs& a, bool gated, hipStream_t s);

@@ -386,7 +386,7 @@ int product8(const fp8adam_product8* p, bool gated, hipStream_t s) {
   if (p->keep_up.codes) a.keep[1] = out8(p->keep_up);
   a.act = p->activation;
   if (packs) {
-    if (packs_itself(a)) {
+    if (packs_itself(a, p->x_in)) {
       a.xin = p->x_in.data;
       a.xin_dt = p->x_in.dtype;
       a.xin_ld = p->x_in.ld;

@@ -372,42 +372,68 @@ __global__ __launch_bounds__(kProdThreads, 2) void k_product(const ProductArgs a
 // Few tokens, nothing kept: bound by the weights' bytes.  A work-group takes 16 rows of
 // weights (gated: 16 of each projection) and its eight waves an eighth of the blocks of 128
 // each, weights straight into registers; their sums meet in shared memory.
-// PACK: up to 16 tokens in 16 or 32 bits, which each wave turns into codes itself as the
-// fragments it needs (the first work-group stores them).
+// PACK: up to 16 tokens in 16 or 32 bits on whole dwords, which each wave turns into codes itself as
+// the fragments it needs, while its weights are on their way (the first work-group stores them).
 constexpr int kFewWaves = 8;
-constexpr int kFewAhead = 4;  // blocks in flight per wave
 
-template <int FMT>
-__device__ __forceinline__ v8i pack_frag(const ProductArgs& a, int64_t t, int k, int g, bool store, int& xs) {
+// The 32 values of lane group g in block k of token t: zeros behind the last token and the row's end.
+template <int DT>
+__device__ __forceinline__ void load_values(Rsrc r, const ProductArgs& a, int64_t t, int k, int g, vu4 (&raw)[DT == FP8ADAM_F32 ? 8 : 4]) {
+  constexpr int kBytes = (int)dtype_bytes(DT);
+  const uint32_t o = t < a.tokens && k * 128 < a.cols ? (uint32_t)(kBytes * (t * a.xin_ld + 128 * k + 32 * g)) : 0x7FFFFF00u;
+#pragma unroll
+  for (int q = 0; q < 2 * kBytes; q++) raw[q] = __builtin_amdgcn_raw_buffer_load_b128(r, o + 16 * q, 0, 0);
+}
+
+template <int DT, int FMT>
+__device__ __forceinline__ v8i pack_values(const ProductArgs& a, int64_t t, int k, int g, bool store,
+                                           const vu4 (&raw)[DT == FP8ADAM_F32 ? 8 : 4], uint32_t& byte) {
   float x[8][4];
-  uint32_t am = 0;
 #pragma unroll
   for (int q = 0; q < 8; q++) {
-    const int64_t c = 128 * (int64_t)k + 32 * g + 4 * q;
-    ld4(a.xin_dt, a.xin, t * a.xin_ld + c, t < a.tokens ? a.cols - c : 0, x[q]);
+    if constexpr (DT == FP8ADAM_F32) unpack4<DT>(Raw4<DT>{raw[q]}, x[q]);
+    else unpack4<DT>(Raw4<DT>{q & 1 ? vu2{raw[q >> 1].z, raw[q >> 1].w} : vu2{raw[q >> 1].x, raw[q >> 1].y}}, x[q]);
+  }
+  if (128 * k + 128 > a.cols) {  // uniform
+#pragma unroll
+    for (int q = 0; q < 8; q++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) x[q][j] = 128 * k + 32 * g + 4 * q + j < a.cols ? x[q][j] : 0.0f;
+  }
+  uint32_t am = 0;
+#pragma unroll
+  for (int q = 0; q < 8; q++)
 #pragma unroll
     for (int j = 0; j < 4; j++) am = max(am, abs_bits(x[q][j]));
-  }
   am = max(am, (uint32_t)__shfl_xor((int)am, 16));
   am = max(am, (uint32_t)__shfl_xor((int)am, 32));
-  float s, inv;
-  choose_scale<FMT, 0>(am, s, inv);
+  byte = scale_byte<FMT>(am);
+  const float s = __uint_as_float(byte << 23);
+  const bool odd = nonfinite_amax(am);
   v8i f;
 #pragma unroll
-  for (int q = 0; q < 8; q++) f[q] = (int)codes4_pow2<FMT>(x[q], s, nonfinite_amax(am));
-  xs = (int)(__float_as_uint(s) >> 23);
+  for (int q = 0; q < 8; q++) f[q] = (int)codes4_pow2<FMT>(x[q], s, false);
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(odd) != 0, 0)) {
+#pragma unroll
+    for (int q = 0; q < 8; q++)
+      if (odd) f[q] = (int)codes4_pow2<FMT>(x[q], 1.0f, true);
+  }
   if (store && t < a.tokens) {
     uint8_t* p = a.x8.codes + t * a.x8.ld + 128 * (int64_t)k + 32 * g;
     st_global<vu4>(p, vu4{(uint32_t)f[0], (uint32_t)f[1], (uint32_t)f[2], (uint32_t)f[3]});
     st_global<vu4>(p + 16, vu4{(uint32_t)f[4], (uint32_t)f[5], (uint32_t)f[6], (uint32_t)f[7]});
-    if (g == 0) st_global<uint8_t>(a.x8.scales + t * a.x8.ld_scale + k, (uint8_t)xs);
+    if (g == 0) st_global<uint8_t>(a.x8.scales + t * a.x8.ld_scale + k, (uint8_t)byte);
   }
   return f;
 }
 
-template <int XF, int WF, bool GATED, int NT, bool PACK>
+// XDT: the type of x that the kernel packs, or kCodes where x is packed already.
+using fp8adam_list::kCodes;
+template <int XF, int WF, bool GATED, int NT, int XDT>
 __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(const ProductArgs a) {
   constexpr int G = GATED ? 2 : 1;
+  constexpr bool PACK = XDT != kCodes;
+  constexpr int kAhead = NT == 1 && XDT != FP8ADAM_F32 ? 4 : 2;  // blocks in flight per wave
   __shared__ vf4_t red[kFewWaves][G][NT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, fr = lane & 15;
@@ -417,7 +443,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(const ProductArg
   Rsrc rw[G];
 #pragma unroll
   for (int p = 0; p < G; p++) rw[p] = rsrc(a.w[p].codes + (int64_t)n0 * a.w[p].ld, vn * a.w[p].ld);
-  const Rsrc rx = rsrc(PACK ? nullptr : a.x.codes, PACK ? 0 : a.tokens * a.x.ld);
+  const Rsrc rx = PACK ? rsrc(a.xin, dtype_bytes(PACK ? XDT : 0) * ((a.tokens - 1) * a.xin_ld + a.cols))
+                       : rsrc(a.x.codes, a.tokens * a.x.ld);
   const int64_t wrow = n0 + min(fr, (int)vn - 1);
 
   vf4_t acc[G][NT];
@@ -430,39 +457,48 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(const ProductArg
     const vu4 a = __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0), b = __builtin_amdgcn_raw_buffer_load_b128(r, o + 16, 0, 0);
     return v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
   };
-  for (int k0 = wave; k0 < nk; k0 += kFewWaves * kFewAhead) {
-    v8i w[kFewAhead][G];
-    int ws[kFewAhead][G];
+  for (int k0 = wave; k0 < nk; k0 += kFewWaves * kAhead) {
+    // x first: loads come back in their order, and x is packed while the weights are on their way
+    vu4 raw[PACK ? kAhead : 1][PACK && XDT == FP8ADAM_F32 ? 8 : 4];
+    v8i x[kAhead][NT], w[kAhead][G];
+    uint32_t xs[kAhead][NT], ws[kAhead][G];
 #pragma unroll
-    for (int u = 0; u < kFewAhead; u++) {
+    for (int u = 0; u < kAhead; u++) {
       const int k = k0 + kFewWaves * u;
+      if constexpr (PACK) {
+        load_values<XDT>(rx, a, fr, k, g, raw[u]);
+      } else {
 #pragma unroll
-      for (int p = 0; p < G; p++) {
-        // behind the last block: outside the resource, zeros
-        w[u][p] = two(rw[p], k < nk ? (uint32_t)fr * (uint32_t)a.w[p].ld + 128u * k + 32u * g : 0x7FFFFF00u);
-        ws[u][p] = (int)(__float_as_uint(scale_at(a.w[p].scales, wrow * a.w[p].ld_scale + min(k, nk - 1), a.w[p].f32)) >> 23);
+        for (int j = 0; j < NT; j++) {
+          const int64_t t = 16 * j + fr;  // behind the last token or block: outside the resource, zeros
+          x[u][j] = two(rx, t < a.tokens && k < nk ? (uint32_t)t * (uint32_t)a.x.ld + 128u * k + 32u * g : 0x7FFFFF00u);
+          xs[u][j] = __float_as_uint(scale_at(a.x.scales, min(t, a.tokens - 1) * a.x.ld_scale + min(k, nk - 1), a.x.f32)) >> 23;
+        }
       }
     }
 #pragma unroll
-    for (int u = 0; u < kFewAhead; u++) {
+    for (int u = 0; u < kAhead; u++) {
       const int k = k0 + kFewWaves * u;
-      if (k >= nk) break;  // the same in the wave
+#pragma unroll
+      for (int p = 0; p < G; p++) {
+        w[u][p] = two(rw[p], k < nk ? (uint32_t)fr * (uint32_t)a.w[p].ld + 128u * k + 32u * g : 0x7FFFFF00u);
+        ws[u][p] = __float_as_uint(scale_at(a.w[p].scales, wrow * a.w[p].ld_scale + min(k, nk - 1), a.w[p].f32)) >> 23;
+      }
+    }
+    if constexpr (PACK) {
+#pragma unroll
+      for (int u = 0; u < kAhead; u++)
+        x[u][0] = pack_values<XDT, XF>(a, fr, k0 + kFewWaves * u, g, blockIdx.x == 0 && k0 + kFewWaves * u < nk, raw[u], xs[u][0]);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; u++) {
       v8bf wide[G][4];
 #pragma unroll
       for (int p = 0; p < G; p++) widen<WF>(w[u][p], ws[u][p], wide[p]);
 #pragma unroll
       for (int j = 0; j < NT; j++) {
-        const int64_t t = 16 * j + fr;
-        int xs;
-        v8i x;
-        if constexpr (PACK) {
-          x = pack_frag<XF>(a, t, k, g, blockIdx.x == 0, xs);
-        } else {
-          x = two(rx, (uint32_t)t * (uint32_t)a.x.ld + 128u * k + 32u * g);
-          xs = t < a.tokens ? (int)(__float_as_uint(scale_at(a.x.scales, t * a.x.ld_scale + k, a.x.f32)) >> 23) : 127;
-        }
         v8bf xw[4];
-        widen<XF>(x, xs, xw);
+        widen<XF>(x[u][j], xs[u][j], xw);
 #pragma unroll
         for (int p = 0; p < G; p++) acc[p][j] = mfma_wide(wide[p], xw, acc[p][j]);
       }
@@ -517,10 +553,14 @@ int launch_tiles(ProductArgs a, hipStream_t s) {
 template <int XF, int WF, bool GATED>
 int launch_few(const ProductArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.rows + 15) / 16)), block(64 * kFewWaves);
-  if (a.xin) return launch(k_product_few<XF, WF, GATED, 1, true>, grid, block, 0, s, a);
-  if (a.tokens <= 16) return launch(k_product_few<XF, WF, GATED, 1, false>, grid, block, 0, s, a);
-  if (a.tokens <= 32) return launch(k_product_few<XF, WF, GATED, 2, false>, grid, block, 0, s, a);
-  return launch(k_product_few<XF, WF, GATED, 4, false>, grid, block, 0, s, a);
+  auto go = [&](auto kernel) { return launch(kernel, grid, block, 0, s, a); };
+  if (a.xin) {
+    if (a.xin_dt == FP8ADAM_F32) return go(k_product_few<XF, WF, GATED, 1, FP8ADAM_F32>);
+    return a.xin_dt == FP8ADAM_BF16 ? go(k_product_few<XF, WF, GATED, 1, FP8ADAM_BF16>) : go(k_product_few<XF, WF, GATED, 1, FP8ADAM_F16>);
+  }
+  if (a.tokens <= 16) return go(k_product_few<XF, WF, GATED, 1, kCodes>);
+  if (a.tokens <= 32) return go(k_product_few<XF, WF, GATED, 2, kCodes>);
+  return go(k_product_few<XF, WF, GATED, 4, kCodes>);
 }
 
 template <int XF, int WF, bool GATED>

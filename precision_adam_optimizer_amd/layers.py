@@ -14,6 +14,7 @@ backward pass calls the functions that end in ``_backward`` or ``_grad8`` itself
 from __future__ import annotations
 
 import ctypes
+from struct import Struct
 from typing import NamedTuple
 
 import torch
@@ -63,7 +64,14 @@ class Grad8Arg(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
+# The same structs packed by the calls below: filling nested ctypes structures costs a small call 5 us.
+_M, _M8 = "Qqii", "QQqqii"
+_PRODUCT8 = Struct("@3q" + _M + 3 * _M8 + 3 * _M + 3 * _M8 + "2i")
+_ACT_BACKWARD8 = Struct("@2q" + _M + 2 * _M8 + 3 * _M + "Qq2i")
+_GRAD8 = Struct("@3q2i" + 2 * _M + 2 * _M8 + _M + "Qq")
+
 _ready = None
+_calls: dict = {}  # the functions on packed structs, by name
 
 
 def _lib() -> ctypes.CDLL:
@@ -82,6 +90,10 @@ def _lib() -> ctypes.CDLL:
                 fn.argtypes = [P(arg)]
         for name in LAYER_EXPORTS:
             getattr(L, name).restype = ctypes.c_int64 if name.endswith("_workspace") else ctypes.c_int
+        for name in LAYER_EXPORTS[2:]:
+            fn = _calls[name[8:]] = L[name]  # another function object
+            fn.argtypes = [ctypes.c_char_p] if name.endswith("_workspace") else [ctypes.c_char_p, vp]
+            fn.restype = getattr(L, name).restype
         _ready = L
     return _ready
 
@@ -158,7 +170,7 @@ class Packed8:
     uint8 or float8_e8m0fnu bytes b that stand for 2^(b - 127), or float32 powers of two, as
     ``Quantizer`` writes them.
     """
-    __slots__ = ("codes", "scales", "rows", "cols", "format", "scale_type")
+    __slots__ = ("_room", "_codes", "_scales", "rows", "cols", "format", "scale_type", "device", "_fields")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: str = "e4m3"):
         self.format = _FP8_FORMATS[codes.dtype] if codes.dtype in _FP8_FORMATS else _FORMATS[fmt]
@@ -184,7 +196,38 @@ class Packed8:
             padded = scales.new_full((self.rows, -(-blocks // 4) * 4), 127)
             padded[:, :blocks] = scales[:, :blocks]
             scales = padded
-        self.codes, self.scales = codes, scales
+        self._codes, self._scales, self.device = codes, scales, codes.device
+        many = self.rows > 1
+        self._fields = (codes.data_ptr(), scales.data_ptr(), codes.stride(0) if many else codes.shape[1],
+                        scales.stride(0) if many else scales.shape[1], self.format, self.scale_type)
+
+    @classmethod
+    def _new(cls, rows: int, cols: int, fmt: str, device) -> "Packed8":
+        """Room for a matrix, codes and scales in one allocation."""
+        p = cls.__new__(cls)
+        blocks = -(-cols // BLOCK)
+        ld, ld_scale = BLOCK * blocks, -(-blocks // 4) * 4
+        p._room = torch.empty(rows * (ld + ld_scale), dtype=torch.uint8, device=device)
+        p._codes = None
+        p.rows, p.cols, p.format, p.scale_type, p.device = rows, cols, _FORMATS[fmt], SCALES_E8M0, device
+        at = p._room.data_ptr()
+        p._fields = (at, at + rows * ld, ld, ld_scale, p.format, SCALES_E8M0)
+        return p
+
+    def _views(self):
+        if self._codes is None:
+            ld, ld_scale = self._fields[2:4]
+            self._codes = self._room.as_strided((self.rows, ld), (ld, 1))
+            self._scales = self._room.as_strided((self.rows, ld_scale), (ld_scale, 1), self.rows * ld)
+        return self._codes, self._scales
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self._views()[0]
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._views()[1]
 
     @classmethod
     def from_quantizer(cls, q, i: int) -> "Packed8":
@@ -202,25 +245,23 @@ class Packed8:
     def fmt(self) -> str:
         return "e4m3" if self.format == E4M3 else "e5m2"
 
-    @property
-    def device(self) -> torch.device:
-        return self.codes.device
-
     def values(self):
         """Views of the codes as float8 [rows, cols] and of the scales, [rows, blocks] (float8_e8m0fnu or float32)."""
-        s = self.scales[:, :-(-self.cols // BLOCK)]
-        return self.codes.view(_FP8[self.format])[:, :self.cols], s if self.scale_type == SCALES_F32 else s.view(torch.float8_e8m0fnu)
+        c, s = self._views()
+        blocks = -(-self.cols // BLOCK)
+        if self.cols != c.shape[1]:
+            c = c[:, :self.cols]
+        if blocks != s.shape[1]:
+            s = s[:, :blocks]
+        return c.view(_FP8[self.format]), s if self.scale_type == SCALES_F32 else s.view(torch.float8_e8m0fnu)
 
     def arg(self) -> tuple:
         """The fields of the C struct."""
-        c, s = self.codes, self.scales
-        if self.rows > 1:
-            return c.data_ptr(), s.data_ptr(), c.stride(0), s.stride(0), self.format, self.scale_type
-        return c.data_ptr(), s.data_ptr(), c.shape[1], s.shape[1], self.format, self.scale_type
+        return self._fields
 
 
-_NO_MATRIX = (None, 0, 0, 0)
-_NO_MATRIX8 = (None, None, 0, 0, 0, 0)
+_NO_MATRIX = (0, 0, 0, 0)
+_NO_MATRIX8 = (0, 0, 0, 0, 0, 0)
 
 
 def _matrix(t: torch.Tensor, what: str) -> torch.Tensor:
@@ -258,7 +299,8 @@ def _vector(t: torch.Tensor, what: str, n: int, device) -> tuple:
 
 def _run(fn, args, device: torch.device) -> None:
     """fn(args, stream) on the device's current stream, with the device current."""
-    _need(device.type == "cuda", "the tensors must be on a GPU")
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a GPU")
     index = device.index
     if torch.cuda.current_device() == index:
         rc = fn(args, torch._C._cuda_getCurrentRawStream(index))
@@ -269,13 +311,20 @@ def _run(fn, args, device: torch.device) -> None:
         _check(rc)
 
 
-def _new8(rows: int, cols: int, fmt: str, device) -> Packed8:
-    p = Packed8.__new__(Packed8)
-    blocks = -(-cols // BLOCK)
-    p.codes = torch.empty((rows, BLOCK * blocks), dtype=torch.uint8, device=device)
-    p.scales = torch.empty((rows, -(-blocks // 4) * 4), dtype=torch.uint8, device=device)
-    p.rows, p.cols, p.format, p.scale_type = rows, cols, _FORMATS[fmt], SCALES_E8M0
-    return p
+def _call_on(name: str, args: bytes, device: torch.device) -> None:
+    if _ready is None:
+        _lib()
+    _run(_calls[name], args, device)
+
+
+def _room(name: str, args: bytes) -> int:
+    """Bytes of workspace that a call needs."""
+    if _ready is None:
+        _lib()
+    n = _calls[name + "_workspace"](args)
+    if n < 0:
+        _check(n)
+    return n
 
 
 def _act(name: str) -> int:
@@ -288,7 +337,7 @@ def _is8(p, what: str, rows: int, cols: int, device) -> Packed8:
     _need(isinstance(p, Packed8), f"{what} must be a Packed8")
     if p.rows != rows or p.cols != cols:
         raise ValueError(f"{what} must have {rows} rows of {cols}")
-    _need(p.codes.device == device, "every tensor must be on one device")
+    _need(p.device == device, "every tensor must be on one device")
     return p
 
 
@@ -296,7 +345,7 @@ def pack8(x: torch.Tensor, fmt: str = "e4m3") -> Packed8:
     """x in 8 bits, by rows of its last dimension: the operand of a product and the checkpoint of its input."""
     m = _matrix(x, "x")
     rows, cols = m.shape
-    out = _new8(rows, cols, fmt, x.device)
+    out = Packed8._new(rows, cols, fmt, x.device)
     a, b = MatrixArg(*_arg(m, "x", rows, cols, x.device)), Matrix8Arg(*out.arg())
     _run(lambda args, stream: _lib().fp8adam_pack8(*args, rows, cols, stream), (ctypes.byref(a), ctypes.byref(b)), x.device)
     return out
@@ -334,7 +383,7 @@ class Gated8(NamedTuple):
 def _product(x, w: Packed8, w_up, bias, act: str, residual, dtype, fmt: str, keep, pack, out):
     gated = w_up is not None
     _need(isinstance(w, Packed8), "the weights must be a Packed8")
-    N, K, device = w.rows, w.cols, w.codes.device
+    N, K, device = w.rows, w.cols, w.device
     if isinstance(x, Packed8):
         T, lead = x.rows, (x.rows,)
         x8, x_in = _is8(x, "x", T, K, device), _NO_MATRIX
@@ -342,21 +391,26 @@ def _product(x, w: Packed8, w_up, bias, act: str, residual, dtype, fmt: str, kee
         m = x if x.dim() == 2 else _matrix(x, "x")
         T, lead = m.shape[0], x.shape[:-1]
         x_in = _arg(m, "x", T, K, device)
-        x8 = _new8(T, K, fmt, device)
+        x8 = Packed8._new(T, K, fmt, device)
     _need(out is not None or dtype is not None or pack is not None, "nothing to write: dtype, out and pack are None")
-    if out is None and dtype is not None:
+    if out is not None:
+        y = _arg(out, "out", T, N, device)
+    elif dtype is not None:
         _need(dtype in _DTYPES, "dtype must be float32, bfloat16 or float16")
         out = torch.empty((*lead, N), dtype=dtype, device=device)
-    y8 = None if pack is None else _new8(T, N, pack, device)
-    z = None if keep is None else _new8(T, N, keep, device)
-    z_up = _new8(T, N, keep, device) if gated and keep is not None else None
-    args = Product8Arg(T, N, K, x_in, x8.arg(), w.arg(), _is8(w_up, "w_up", N, K, device).arg() if gated else _NO_MATRIX8,
-                       _NO_MATRIX if bias is None else _vector(bias, "bias", N, device),
-                       _NO_MATRIX if residual is None else _arg(residual, "residual", T, N, device),
-                       _NO_MATRIX if out is None else _arg(out, "out", T, N, device),
-                       _NO_MATRIX8 if y8 is None else y8.arg(), _NO_MATRIX8 if z is None else z.arg(),
-                       _NO_MATRIX8 if z_up is None else z_up.arg(), _act(act), 0)
-    _run(_lib().fp8adam_gated8 if gated else _lib().fp8adam_linear8, args, device)
+        y = (out.data_ptr(), N, _DTYPES[dtype], 0)
+    else:
+        y = _NO_MATRIX
+    y8 = None if pack is None else Packed8._new(T, N, pack, device)
+    z = None if keep is None else Packed8._new(T, N, keep, device)
+    z_up = Packed8._new(T, N, keep, device) if gated and keep is not None else None
+    args = _PRODUCT8.pack(
+        T, N, K, *x_in, *x8._fields, *w._fields, *(_is8(w_up, "w_up", N, K, device)._fields if gated else _NO_MATRIX8),
+        *(_NO_MATRIX if bias is None else _vector(bias, "bias", N, device)),
+        *(_NO_MATRIX if residual is None else _arg(residual, "residual", T, N, device)), *y,
+        *(_NO_MATRIX8 if y8 is None else y8._fields), *(_NO_MATRIX8 if z is None else z._fields),
+        *(_NO_MATRIX8 if z_up is None else z_up._fields), _act(act), 0)
+    _call_on("gated8" if gated else "linear8", args, device)
     return out, x8, z, z_up, y8
 
 
@@ -388,9 +442,9 @@ def gated8_backward(dy: torch.Tensor, gate: Packed8, up: Packed8, *, activation:
     ``outs``: the two tensors to write, of which one may be dy itself."""
     T, N, device = gate.rows, gate.cols, gate.device
     dgate, dup = (torch.empty_like(dy, memory_format=torch.contiguous_format) for _ in range(2)) if outs is None else outs
-    args = ActBackward8Arg(T, N, _arg(dy, "dy", T, N, device), gate.arg(), _is8(up, "up", T, N, device).arg(),
-                           _arg(dgate, "dgate", T, N, device), _arg(dup, "dup", T, N, device), _NO_MATRIX, None, 0, 0, _act(activation))
-    _run(_lib().fp8adam_gated8_backward, args, device)
+    args = _ACT_BACKWARD8.pack(T, N, *_arg(dy, "dy", T, N, device), *gate._fields, *_is8(up, "up", T, N, device)._fields,
+                               *_arg(dgate, "dgate", T, N, device), *_arg(dup, "dup", T, N, device), *_NO_MATRIX, 0, 0, 0, _act(activation))
+    _call_on("gated8_backward", args, device)
     return dgate, dup
 
 
@@ -412,34 +466,29 @@ def linear8_backward(dy: torch.Tensor, z: Packed8 | None = None, *, activation: 
         out = dy
     elif out is None:
         out = torch.empty_like(dy, memory_format=torch.contiguous_format)
-    args = ActBackward8Arg(T, N, _arg(m, "dy", T, N, device), _NO_MATRIX8 if none else _is8(z, "z", T, N, device).arg(), _NO_MATRIX8,
-                           _NO_MATRIX if none else _arg(out, "out", T, N, device), _NO_MATRIX,
-                           _NO_MATRIX if bias_grad is None else _vector(bias_grad, "bias_grad", N, device), None, 0, int(accumulate), act)
-    space = None
-    if bias_grad is not None:
-        space = _workspace(fp8adam_linear8_backward_workspace(args), args, device)
-    _run(_lib().fp8adam_linear8_backward, args, device)
-    del space
+    fields = (T, N, *_arg(m, "dy", T, N, device), *(_NO_MATRIX8 if none else _is8(z, "z", T, N, device)._fields), *_NO_MATRIX8,
+              *(_NO_MATRIX if none else _arg(out, "out", T, N, device)), *_NO_MATRIX,
+              *(_NO_MATRIX if bias_grad is None else _vector(bias_grad, "bias_grad", N, device)))
+    _with_room("linear8_backward", _ACT_BACKWARD8, fields, (int(accumulate), act), device, bias_grad is not None)
     return out
 
 
-def _workspace(n: int, args, device):
-    """Room for a call, which torch hands out again in the order of the stream."""
-    if n == 0:
-        return None
-    space = torch.empty(n, dtype=torch.uint8, device=device)
-    args.workspace, args.workspace_bytes = space.data_ptr(), n
-    return space
+def _with_room(name: str, struct: Struct, before: tuple, after: tuple, device: torch.device, asks: bool = True) -> None:
+    """A call with the workspace it needs, which torch hands out again in the order of the stream."""
+    args = struct.pack(*before, 0, 0, *after)
+    n = _room(name, args) if asks else 0
+    if n:
+        space = torch.empty(n, dtype=torch.uint8, device=device)
+        args = struct.pack(*before, space.data_ptr(), n, *after)
+    _call_on(name, args, device)
 
 
 def _grad(name: str, dys, bs, out, T: int, N: int, K: int, rows: int, accumulate: bool) -> torch.Tensor:
     device = bs[0].device
-    args = Grad8Arg(T, N, K, len(dys), int(accumulate), tuple(_arg(d, "dy", T, N, device) for d in dys), tuple(b.arg() for b in bs),
-                    _arg(out, "out", rows, K, device), None, 0)
-    L = _lib()
-    space = _workspace(_bytes(f"fp8adam_{name}_workspace", args), args, device)
-    _run(getattr(L, f"fp8adam_{name}"), args, device)
-    del space
+    two = len(dys) == 2
+    before = (T, N, K, len(dys), int(accumulate), *_arg(dys[0], "dy", T, N, device), *(_arg(dys[1], "dy", T, N, device) if two else _NO_MATRIX),
+              *bs[0]._fields, *(bs[1]._fields if two else _NO_MATRIX8), *_arg(out, "out", rows, K, device))
+    _with_room(name, _GRAD8, before, (), device)
     return out
 
 
