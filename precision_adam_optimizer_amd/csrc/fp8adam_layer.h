@@ -340,7 +340,7 @@ struct ProductArgs {
 
 // The kernel for few tokens, which keeps nothing in 8 bits (a block of 128 outputs spans its
 // work-groups); with the fewest it packs x itself.
-constexpr int kFewTokens = 64, kFewPackTokens = 16;
+constexpr int kFewTokens = 64, kFewPackTokens = 4;
 inline bool few_tokens(const ProductArgs& a) {
   return a.tokens <= kFewTokens && !a.keep[0].codes && !a.keep[1].codes && !a.y8.codes;
 }

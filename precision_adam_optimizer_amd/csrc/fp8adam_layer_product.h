@@ -370,71 +370,27 @@ __global__ __launch_bounds__(kProdThreads, 2) void k_product(const ProductArgs a
 }
 
 // Few tokens, nothing kept: bound by the weights' bytes.  A work-group takes 16 rows of
-// weights (gated: 16 of each projection) and its eight waves an eighth of the blocks of 128
-// each, weights straight into registers; their sums meet in shared memory.
-// PACK: up to 16 tokens in 16 or 32 bits on whole dwords, which each wave turns into codes itself as
-// the fragments it needs, while its weights are on their way (the first work-group stores them).
-constexpr int kFewWaves = 8;
-
-// The 32 values of lane group g in block k of token t: zeros behind the last token and the row's end.
-template <int DT>
-__device__ __forceinline__ void load_values(Rsrc r, const ProductArgs& a, int64_t t, int k, int g, vu4 (&raw)[DT == FP8ADAM_F32 ? 8 : 4]) {
-  constexpr int kBytes = (int)dtype_bytes(DT);
-  const uint32_t o = t < a.tokens && k * 128 < a.cols ? (uint32_t)(kBytes * (t * a.xin_ld + 128 * k + 32 * g)) : 0x7FFFFF00u;
-#pragma unroll
-  for (int q = 0; q < 2 * kBytes; q++) raw[q] = __builtin_amdgcn_raw_buffer_load_b128(r, o + 16 * q, 0, 0);
-}
-
-template <int DT, int FMT>
-__device__ __forceinline__ v8i pack_values(const ProductArgs& a, int64_t t, int k, int g, bool store,
-                                           const vu4 (&raw)[DT == FP8ADAM_F32 ? 8 : 4], uint32_t& byte) {
-  float x[8][4];
-#pragma unroll
-  for (int q = 0; q < 8; q++) {
-    if constexpr (DT == FP8ADAM_F32) unpack4<DT>(Raw4<DT>{raw[q]}, x[q]);
-    else unpack4<DT>(Raw4<DT>{q & 1 ? vu2{raw[q >> 1].z, raw[q >> 1].w} : vu2{raw[q >> 1].x, raw[q >> 1].y}}, x[q]);
-  }
-  if (128 * k + 128 > a.cols) {  // uniform
-#pragma unroll
-    for (int q = 0; q < 8; q++)
-#pragma unroll
-      for (int j = 0; j < 4; j++) x[q][j] = 128 * k + 32 * g + 4 * q + j < a.cols ? x[q][j] : 0.0f;
-  }
-  uint32_t am = 0;
-#pragma unroll
-  for (int q = 0; q < 8; q++)
-#pragma unroll
-    for (int j = 0; j < 4; j++) am = max(am, abs_bits(x[q][j]));
-  am = max(am, (uint32_t)__shfl_xor((int)am, 16));
-  am = max(am, (uint32_t)__shfl_xor((int)am, 32));
-  byte = scale_byte<FMT>(am);
-  const float s = __uint_as_float(byte << 23);
-  const bool odd = nonfinite_amax(am);
-  v8i f;
-#pragma unroll
-  for (int q = 0; q < 8; q++) f[q] = (int)codes4_pow2<FMT>(x[q], s, false);
-  if (__builtin_expect(__builtin_amdgcn_ballot_w64(odd) != 0, 0)) {
-#pragma unroll
-    for (int q = 0; q < 8; q++)
-      if (odd) f[q] = (int)codes4_pow2<FMT>(x[q], 1.0f, true);
-  }
-  if (store && t < a.tokens) {
-    uint8_t* p = a.x8.codes + t * a.x8.ld + 128 * (int64_t)k + 32 * g;
-    st_global<vu4>(p, vu4{(uint32_t)f[0], (uint32_t)f[1], (uint32_t)f[2], (uint32_t)f[3]});
-    st_global<vu4>(p + 16, vu4{(uint32_t)f[4], (uint32_t)f[5], (uint32_t)f[6], (uint32_t)f[7]});
-    if (g == 0) st_global<uint8_t>(a.x8.scales + t * a.x8.ld_scale + k, (uint8_t)byte);
-  }
-  return f;
-}
-
+// weights (gated: 16 of each projection); in every chunk of the blocks of 128 columns each of its
+// waves takes four (with more than 16 tokens two), weights straight into registers, and the
+// waves' sums meet in shared memory at the end.  Four waves, of which three work-groups share a CU
+// and load while others multiply, or eight where there are too few work-groups for that.
+// PACK: up to 4 tokens in 16 or 32 bits on whole dwords.  The work-group turns a chunk of them into codes
+// in shared memory, 16 lanes a block, while its weights are on their way (the first work-group stores
+// them too).  (One launch less, 5 us; packed by each wave into its own fragments, 15 of whose 16
+// lanes have nothing to do for one token, one token x 4096 x 2 * 11008 took 36 us.  Every work-group
+// packs every token, so with more of them a launch of its own is faster.)
 // XDT: the type of x that the kernel packs, or kCodes where x is packed already.
 using fp8adam_list::kCodes;
-template <int XF, int WF, bool GATED, int NT, int XDT>
-__global__ __launch_bounds__(64 * kFewWaves) void k_product_few(const ProductArgs a) {
+template <int XF, int WF, bool GATED, int NT, int XDT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 2) void k_product_few(const ProductArgs a) {
   constexpr int G = GATED ? 2 : 1;
   constexpr bool PACK = XDT != kCodes;
-  constexpr int kAhead = NT == 1 && XDT != FP8ADAM_F32 ? 4 : 2;  // blocks in flight per wave
-  __shared__ vf4_t red[kFewWaves][G][NT][64];
+  constexpr int kAhead = NT > 1 ? 2 : 4;        // blocks of a wave in a chunk
+  constexpr int kBlocks = WAVES * kAhead;       // of a chunk
+  constexpr int kLd = kBlocks * 128 + 16;       // bytes between tokens in shared memory: spread over the banks
+  __shared__ vf4_t red[WAVES][G][NT][64];
+  __shared__ __attribute__((aligned(16))) uint8_t packed[PACK ? 16 * kLd : 16];
+  __shared__ uint8_t bytes[PACK ? 16 : 1][kBlocks];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, fr = lane & 15;
   const int n0 = blockIdx.x * 16;
@@ -454,55 +410,124 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(const ProductArg
     for (int j = 0; j < NT; j++) acc[p][j] = vf4_t{0, 0, 0, 0};
 
   auto two = [](Rsrc r, uint32_t o) {
-    const vu4 a = __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0), b = __builtin_amdgcn_raw_buffer_load_b128(r, o + 16, 0, 0);
+    const vu4 a = __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0), b = __builtin_amdgcn_raw_buffer_load_b128(r, o + 64, 0, 0);
     return v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
   };
-  for (int k0 = wave; k0 < nk; k0 += kFewWaves * kAhead) {
-    // x first: loads come back in their order, and x is packed while the weights are on their way
-    vu4 raw[PACK ? kAhead : 1][PACK && XDT == FP8ADAM_F32 ? 8 : 4];
+  // x to 8 bits: item i is block i % 16 of token i / 16, for 16 lanes
+  constexpr int kEl = PACK ? (int)dtype_bytes(XDT) : 2;
+  const int items = (int)a.tokens * kBlocks, hl = threadIdx.x & 15;
+  struct Raw8 {
+    vu4 x[kEl / 2];
+  };
+  auto load_x = [&](int kc, int i) __attribute__((always_inline)) {
+    const int k = kc + i % kBlocks;
+    Raw8 r;
+    const uint32_t o = i < items && k < nk ? (uint32_t)(kEl * (i / kBlocks * a.xin_ld + 128 * k + 8 * hl)) : 0x7FFFFF00u;
+#pragma unroll
+    for (int q = 0; q < kEl / 2; q++) r.x[q] = __builtin_amdgcn_raw_buffer_load_b128(rx, o + 16 * q, 0, 0);
+    return r;
+  };
+  auto pack_x = [&](int kc, int i, const Raw8& r) __attribute__((always_inline)) {
+    const int tok = i / kBlocks, blk = i % kBlocks, k = kc + blk;
+    float lo[4], hi[4];
+    constexpr int DT = PACK ? XDT : FP8ADAM_BF16;
+    if constexpr (DT == FP8ADAM_F32) {
+      unpack4<DT>(Raw4<DT>{r.x[0]}, lo);
+      unpack4<DT>(Raw4<DT>{r.x[kEl / 2 - 1]}, hi);
+    } else {
+      unpack4<DT>(Raw4<DT>{vu2{r.x[0].x, r.x[0].y}}, lo);
+      unpack4<DT>(Raw4<DT>{vu2{r.x[0].z, r.x[0].w}}, hi);
+    }
+    uint32_t am = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {  // (a load behind the row's end gives the next row's values)
+      lo[j] = 128 * k + 8 * hl + j < a.cols ? lo[j] : 0.0f;
+      hi[j] = 128 * k + 8 * hl + 4 + j < a.cols ? hi[j] : 0.0f;
+      am = max(am, max(abs_bits(lo[j]), abs_bits(hi[j])));
+    }
+    am = row_max(am);
+    const uint32_t byte = scale_byte<XF>(am);
+    const float s = __uint_as_float(byte << 23);
+    const bool odd = nonfinite_amax(am);
+    vu2 c{codes4_pow2<XF>(lo, s, false), codes4_pow2<XF>(hi, s, false)};
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(odd) != 0, 0)) {
+      if (odd) c = vu2{codes4_pow2<XF>(lo, 1.0f, true), codes4_pow2<XF>(hi, 1.0f, true)};
+    }
+    if (i >= items) return;
+    *reinterpret_cast<vu2*>(packed + tok * kLd + 128 * blk + 8 * hl) = c;
+    if (hl == 0) bytes[tok][blk] = (uint8_t)byte;
+    if (blockIdx.x == 0 && k < nk) {
+      st_global<vu2>(a.x8.codes + tok * a.x8.ld + 128 * (int64_t)k + 8 * hl, c);
+      if (hl == 0) st_global<uint8_t>(a.x8.scales + tok * a.x8.ld_scale + k, (uint8_t)byte);
+    }
+  };
+
+  constexpr int kGroups = WAVES * 4, kItems = PACK ? kFewPackTokens * kBlocks / kGroups : 1;  // of 16 lanes, at most
+  const int first = threadIdx.x >> 4;
+  struct Chunk {
+    Raw8 raw[kItems];
     v8i x[kAhead][NT], w[kAhead][G];
     uint32_t xs[kAhead][NT], ws[kAhead][G];
+  };
+  // x first: loads come back in their order, and x is packed while the weights are on their way
+  auto load = [&](Chunk& c, int kc) __attribute__((always_inline)) {
+    if constexpr (PACK) {
 #pragma unroll
-    for (int u = 0; u < kAhead; u++) {
-      const int k = k0 + kFewWaves * u;
-      if constexpr (PACK) {
-        load_values<XDT>(rx, a, fr, k, g, raw[u]);
-      } else {
+      for (int i = 0; i < kItems; i++) c.raw[i] = load_x(kc, first + kGroups * i);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kAhead; u++) {
+        const int k = kc + wave + WAVES * u;
 #pragma unroll
         for (int j = 0; j < NT; j++) {
           const int64_t t = 16 * j + fr;  // behind the last token or block: outside the resource, zeros
-          x[u][j] = two(rx, t < a.tokens && k < nk ? (uint32_t)t * (uint32_t)a.x.ld + 128u * k + 32u * g : 0x7FFFFF00u);
-          xs[u][j] = __float_as_uint(scale_at(a.x.scales, min(t, a.tokens - 1) * a.x.ld_scale + min(k, nk - 1), a.x.f32)) >> 23;
+          c.x[u][j] = two(rx, t < a.tokens && k < nk ? (uint32_t)t * (uint32_t)a.x.ld + 128u * k + 16u * g : 0x7FFFFF00u);
+          c.xs[u][j] = __float_as_uint(scale_at(a.x.scales, min(t, a.tokens - 1) * a.x.ld_scale + min(k, nk - 1), a.x.f32)) >> 23;
         }
       }
     }
 #pragma unroll
     for (int u = 0; u < kAhead; u++) {
-      const int k = k0 + kFewWaves * u;
+      const int k = kc + wave + WAVES * u;
 #pragma unroll
       for (int p = 0; p < G; p++) {
-        w[u][p] = two(rw[p], k < nk ? (uint32_t)fr * (uint32_t)a.w[p].ld + 128u * k + 32u * g : 0x7FFFFF00u);
-        ws[u][p] = __float_as_uint(scale_at(a.w[p].scales, wrow * a.w[p].ld_scale + min(k, nk - 1), a.w[p].f32)) >> 23;
+        c.w[u][p] = two(rw[p], k < nk ? (uint32_t)fr * (uint32_t)a.w[p].ld + 128u * k + 16u * g : 0x7FFFFF00u);
+        c.ws[u][p] = __float_as_uint(scale_at(a.w[p].scales, wrow * a.w[p].ld_scale + min(k, nk - 1), a.w[p].f32)) >> 23;
       }
     }
+  };
+  auto multiply = [&](Chunk& c, int kc) __attribute__((always_inline)) {
     if constexpr (PACK) {
 #pragma unroll
-      for (int u = 0; u < kAhead; u++)
-        x[u][0] = pack_values<XDT, XF>(a, fr, k0 + kFewWaves * u, g, blockIdx.x == 0 && k0 + kFewWaves * u < nk, raw[u], xs[u][0]);
+      for (int i = 0; i < kItems; i++)
+        if (kGroups * i < items) pack_x(kc, first + kGroups * i, c.raw[i]);
+      stage_barrier<63>();
+#pragma unroll
+      for (int u = 0; u < kAhead; u++) {
+        const uint8_t* p = packed + fr * kLd + 128 * (wave + WAVES * u) + 16 * g;
+        c.x[u][0] = frag(p, 0, 64);  // (behind the last token whatever lies there: it reaches no other)
+        c.xs[u][0] = bytes[fr][wave + WAVES * u];
+      }
     }
 #pragma unroll
     for (int u = 0; u < kAhead; u++) {
       v8bf wide[G][4];
 #pragma unroll
-      for (int p = 0; p < G; p++) widen<WF>(w[u][p], ws[u][p], wide[p]);
+      for (int p = 0; p < G; p++) widen<WF>(c.w[u][p], c.ws[u][p], wide[p]);
 #pragma unroll
       for (int j = 0; j < NT; j++) {
         v8bf xw[4];
-        widen<XF>(x[u][j], xs[u][j], xw);
+        widen<XF>(c.x[u][j], c.xs[u][j], xw);
 #pragma unroll
         for (int p = 0; p < G; p++) acc[p][j] = mfma_wide(wide[p], xw, acc[p][j]);
       }
     }
+    if constexpr (PACK) stage_barrier<63>();  // the codes have been read
+  };
+  for (int kc = 0; kc < nk; kc += kBlocks) {
+    Chunk c;
+    load(c, kc);
+    multiply(c, kc);
   }
 #pragma unroll
   for (int p = 0; p < G; p++)
@@ -518,7 +543,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(const ProductArg
   for (int p = 0; p < G; p++) {
     vf4_t s = red[0][p][wave][lane];
 #pragma unroll
-    for (int k = 1; k < kFewWaves; k++) s += red[k][p][wave][lane];
+    for (int k = 1; k < WAVES; k++) s += red[k][p][wave][lane];
     z[p][0] = s.x, z[p][1] = s.y, z[p][2] = s.z, z[p][3] = s.w;
   }
   if (!GATED && a.bias) {
@@ -527,8 +552,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(const ProductArg
 #pragma unroll
     for (int e = 0; e < 4; e++) z[0][e] += b[e];
   }
-  float (&first)[1][4] = reinterpret_cast<float (&)[1][4]>(z[0]);
-  act_all(a.act, first);
+  float (&one)[1][4] = reinterpret_cast<float (&)[1][4]>(z[0]);
+  act_all(a.act, one);
   if constexpr (GATED) {
 #pragma unroll
     for (int e = 0; e < 4; e++) z[0][e] *= z[G - 1][e];
@@ -550,22 +575,22 @@ int launch_tiles(ProductArgs a, hipStream_t s) {
   return launch(k_product<XF, WF, GATED, TT, WIDE>, dim3((unsigned)((total + 7) / 8 * 8)), dim3(kProdThreads), 0, s, a);
 }
 
-template <int XF, int WF, bool GATED>
+template <int XF, int WF, bool GATED, int WAVES>
 int launch_few(const ProductArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.rows + 15) / 16)), block(64 * kFewWaves);
-  auto go = [&](auto kernel) { return launch(kernel, grid, block, 0, s, a); };
+  auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)((a.rows + 15) / 16)), dim3(64 * WAVES), 0, s, a); };
   if (a.xin) {
-    if (a.xin_dt == FP8ADAM_F32) return go(k_product_few<XF, WF, GATED, 1, FP8ADAM_F32>);
-    return a.xin_dt == FP8ADAM_BF16 ? go(k_product_few<XF, WF, GATED, 1, FP8ADAM_BF16>) : go(k_product_few<XF, WF, GATED, 1, FP8ADAM_F16>);
+    if (a.xin_dt == FP8ADAM_F32) return go(k_product_few<XF, WF, GATED, 1, FP8ADAM_F32, WAVES>);
+    if (a.xin_dt == FP8ADAM_BF16) return go(k_product_few<XF, WF, GATED, 1, FP8ADAM_BF16, WAVES>);
+    return go(k_product_few<XF, WF, GATED, 1, FP8ADAM_F16, WAVES>);
   }
-  if (a.tokens <= 16) return go(k_product_few<XF, WF, GATED, 1, kCodes>);
-  if (a.tokens <= 32) return go(k_product_few<XF, WF, GATED, 2, kCodes>);
-  return go(k_product_few<XF, WF, GATED, 4, kCodes>);
+  if (a.tokens <= 16) return go(k_product_few<XF, WF, GATED, 1, kCodes, WAVES>);
+  if (a.tokens <= 32) return go(k_product_few<XF, WF, GATED, 2, kCodes, WAVES>);
+  return go(k_product_few<XF, WF, GATED, 4, kCodes, WAVES>);
 }
 
 template <int XF, int WF, bool GATED>
 int launch_product_of(const ProductArgs& a, hipStream_t s) {
-  if (few_tokens(a)) return launch_few<XF, WF, GATED>(a, s);
+  if (few_tokens(a)) return a.rows >= 16 * 512 ? launch_few<XF, WF, GATED, 4>(a, s) : launch_few<XF, WF, GATED, 8>(a, s);
   if (a.y && a.y_dt == FP8ADAM_F32) return launch_tiles<XF, WF, GATED, 128, true>(a, s);
   // the tile whose rounds over 256 CUs cost least: a tile of 128 and of 64 tokens takes about 0.6 and
   // 0.4 of the time of one of 256
