@@ -31,15 +31,22 @@ __global__ __launch_bounds__(kThreads) void k_pack(const void* x, int64_t ld, Ou
   const int64_t first = (int64_t)blockIdx.x * kPackBlocks + (threadIdx.x >> 4), total = rows * nb;
   float v[kPackUnroll][8];
   int64_t row[kPackUnroll], blk[kPackUnroll];
-  bool there[kPackUnroll];
+  bool there[kPackUnroll], inside = true;
 #pragma unroll
   for (int u = 0; u < kPackUnroll; u++) {
     const int64_t i = first + u * (kThreads / 16);
     there[u] = i < total;
-    row[u] = total >> 32 ? i / nb : (uint32_t)i / (uint32_t)nb;
-    blk[u] = i - row[u] * nb;
-    const int64_t c = 128 * blk[u] + 8 * lane;
-    ld8<DT>(x, row[u] * ld + c, there[u] ? cols - c : 0, v[u]);
+    const int64_t in = min(i, total - 1);
+    row[u] = total >> 32 ? in / nb : (uint32_t)in / (uint32_t)nb;
+    blk[u] = in - row[u] * nb;
+    inside = inside && 128 * blk[u] + 8 * lane + 8 <= cols;
+  }
+  if (inside) {  // no branch between the loads: all are on their way at once
+#pragma unroll
+    for (int u = 0; u < kPackUnroll; u++) ld8<DT>(x, row[u] * ld + 128 * blk[u] + 8 * lane, 8, v[u]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kPackUnroll; u++) ld8<DT>(x, row[u] * ld + 128 * blk[u] + 8 * lane, cols - 128 * blk[u] - 8 * lane, v[u]);
   }
   put_blocks(o, row, blk, there, lane, v);
 }
@@ -98,7 +105,8 @@ struct ActArgs {
 constexpr int kActRows = 64;  // of a work-group
 
 // One block of 128 columns of kActRows rows, eight columns per lane: reads and writes at once, bound
-// by HBM.  The sums over the rows, for the bias, are added up in fp32 by each lane and then over
+// by HBM (4096 x 11008 gated in bf16: 71 us, 5.0 TB/s).  Each row is loaded when the one before has
+// been written; all four loaded first took 77 us (twice the registers, half the waves).  The sums over the rows, for the bias, are added up in fp32 by each lane and then over
 // the work-group's 16 rows of lanes, always in the same order; k_bias_join adds the chunks.
 template <bool GATED, int ACT, int DT>
 __global__ __launch_bounds__(kThreads) void k_act_backward(const ActArgs a) {
@@ -608,14 +616,33 @@ auto guarded(const char* what, F&& body) -> decltype(body()) {
 
 }  // namespace
 
+// The tiles and the number of parts of the sum whose estimated time is least, in us: 64 of the sum
+// take a work-group of 256 x 256 (one on a CU) 2, one of 128 x 128 1, or 1.35 where there are two on
+// a CU; the parts are written and read again at about 5 TB/s, by one launch more.  (The estimates are
+// within 15% of what was measured, and their order right: 2048 x 2048 x 2048 as 128 x 128 in one
+// part 45 estimated 38, as 256 x 256 in four parts 51 estimated 53; 2048 tokens x 2 pairs of 2048 x 768
+// as 128 x 128 in five parts 35 estimated 40, as 256 x 256 in eight 40 estimated 46; 16384 tokens
+// x 2048 x 768 as 256 x 256 in ten parts 80 estimated 87, as 128 x 128 in five 88 estimated 93.)
 GradPlan plan_grad(int64_t m, int64_t k, int64_t r, int npairs) {
-  const int64_t steps = (r + 63) / 64 * npairs;  // of two stages
-  auto tiles = [&](int64_t t) { return std::max<int64_t>(1, (m + t - 1) / t * ((k + t - 1) / t)); };
-  auto parts = [&](int64_t t, int64_t slots) { return std::max<int64_t>(1, std::min<int64_t>(slots / tiles(t), steps / 8)); };
-  GradPlan p{0, (int)parts(256, 256), 0};
-  if (tiles(256) * p.splits < 192) p = GradPlan{1, (int)parts(128, 512), 0};
-  if (p.splits > 1) p.partial_bytes = p.splits * m * ((k + 3) & ~(int64_t)3) * (int64_t)sizeof(float);
-  return p;
+  const int64_t steps = (r + 63) / 64 * npairs, ldp = (k + 3) & ~(int64_t)3;
+  GradPlan best{0, 1, 0};
+  double least = 0.0;
+  for (int tile = 0; tile < 2; tile++) {
+    const int64_t size = tile ? 128 : 256, slots = tile ? 512 : 256;
+    const int64_t tiles = std::max<int64_t>(1, (m + size - 1) / size * ((k + size - 1) / size));
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(slots / tiles, steps / 2));
+    for (int64_t splits = 1; splits <= most; splits++) {
+      const int64_t groups = tiles * splits;
+      const double step = tile ? (groups > 256 ? 1.35 : 1.0) : 2.0;
+      double t = (double)((groups + slots - 1) / slots) * (double)((steps + splits - 1) / splits) * step;
+      if (splits > 1) t += 4.0 + 8.0 * (double)(splits * m * ldp) / 5e6;
+      if (tile + splits == 1 || t < least) {
+        least = t;
+        best = GradPlan{tile, (int)splits, splits > 1 ? splits * m * ldp * (int64_t)sizeof(float) : 0};
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace fp8adam_layer
