@@ -45,8 +45,8 @@ typedef enum { FP8ADAM_SCALES_E8M0 = 0, FP8ADAM_SCALES_F32 = 1 } fp8adam_scale_t
 #define FP8ADAM_LAYER_MAX_COLS (1 << 20) /* rows and cols of weights, columns of activations */
 #define FP8ADAM_LAYER_MAX_LD (1 << 21)   /* every ld */
 
-/* A matrix in 16 or 32 bits, row-major: rows `ld` elements apart, aligned to its element.  data = NULL
- * where it is optional: absent. */
+/* A matrix in 16 or 32 bits, row-major: rows `ld` elements apart (not used where there is
+ * one row), aligned to its element.  data = NULL where it is optional: absent. */
 typedef struct {
     void *data;
     int64_t ld;

@@ -497,9 +497,10 @@ struct Left {
 
 Left left_of(const fp8adam_matrix& dy, int64_t tokens, int64_t rows) {
   Left l{};
-  l.direct = dy.dtype == FP8ADAM_BF16 && rows % 8 == 0 && dy.ld % 8 == 0 && ((uintptr_t)dy.data & 15u) == 0;
+  const int64_t ld = tokens > 1 ? dy.ld : rows;  // one row's is not used
+  l.direct = dy.dtype == FP8ADAM_BF16 && rows % 8 == 0 && ld % 8 == 0 && ((uintptr_t)dy.data & 15u) == 0;
   l.parts = dy.dtype == FP8ADAM_BF16 ? 1 : 2;
-  l.ld = l.direct ? dy.ld : (rows + 7) & ~(int64_t)7;
+  l.ld = l.direct ? ld : (rows + 7) & ~(int64_t)7;
   l.bytes = l.direct ? 0 : (tokens * l.ld * 2 + 255) & ~(int64_t)255;
   return l;
 }
@@ -521,7 +522,7 @@ int grad_call(const fp8adam_grad8* p, bool weights, GradCall& c) {
   c.direct = true;
   for (int i = 0; i < p->n; i++) {
     c.left[i] = left_of(p->dy[i], p->tokens, p->rows);
-    c.direct = c.direct && c.left[i].direct && p->dy[i].ld == p->dy[0].ld;
+    c.direct = c.direct && c.left[i].direct && c.left[i].ld == c.left[0].ld;
   }
   c.bytes = 0;
   if (!c.direct)
@@ -589,7 +590,7 @@ int grad8(const fp8adam_grad8* p, bool weights, hipStream_t s) {
       ws += l.parts * l.bytes;
     }
   }
-  a.lda = c.direct ? p->dy[0].ld : c.left[0].ld;
+  a.lda = c.left[0].ld;
   a.trans = weights;
   a.m = weights ? N : T;
   a.r = weights ? T : N;
