@@ -58,7 +58,7 @@ typedef struct {
  * rounded up to 128; the codes behind cols, up to that multiple, are zero (written as zero by the calls
  * that write such a matrix).  scales: rows `ld_scale` entries apart, 4-byte aligned.  E8M0: bytes b that
  * stand for 2^(b - 127), ld_scale a multiple of 4.  F32: powers of two in fp32 (of matrices that a call
- * reads only).  codes = NULL where it is optional: absent. */
+ * reads only).  Scales lie between 2^-126 and 2^127 (b between 1 and 254); others are not checked for.  codes = NULL where it is optional: absent. */
 typedef struct {
     void *codes;
     void *scales;

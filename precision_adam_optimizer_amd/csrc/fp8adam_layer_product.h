@@ -2,9 +2,9 @@
 // for each pair of formats in fp8adam_layer_product_*.hip.
 //
 // Both operands are codes with one power-of-two scale per row and 128 columns, and
-// gfx950's scaled matrix instruction multiplies 32 x 64 by 64 x 32 codes with a scale for
-// every row and 32 columns: two instructions take exactly one block of 32 rows of
-// each, with its scales.
+// gfx950's scaled matrix instruction multiplies 16 x 128 by 128 x 16 codes with a scale for
+// every row and 32 columns: one instruction takes exactly one block of 16 rows of each, with
+// its scales.  (As 32 x 64 by 64 x 32 it reached 8% less on the whole card.)
 //
 // The instruction sums eight consecutive products at a time, each cut (towards zero) at 2^-13 of the
 // power of two of the largest product's exponents, and adds these sums to 32 bits (measured with
@@ -117,6 +117,12 @@ __device__ __forceinline__ void put_scales(const void* scales, bool f32, int64_t
 // The sums then go through shared memory, 32 tokens of each wave at a time, into rows of
 // 128 columns for 16 lanes each: bias, activation, product, residual and the blocks' amax
 // are made there, and whole lines are stored.
+//
+// Measured (E4M3, SiLU, both projections kept): 4096 tokens x 4096 x 2 * 11008 in 330 us, 2240 TFLOP/s;
+// 8192 x 4096 x 4096 with a residual in 135 us, 2040; 8192^3 without in 2.8 PFLOP/s, where the
+// card's power is what bounds it (a loop of the instruction alone reaches 3.9 to 4.5).  What is lost
+// against that is each tile's start, 9K cycles until its first operands and scales are there, and its end,
+// 7K to 12K cycles of activation and rounding, in which its CU does not multiply.
 template <int XF, int WF, bool GATED, int TT, bool WIDE>
 __global__ __launch_bounds__(kProdThreads, 2) void k_product(const ProductArgs a) {
   constexpr int WN = TT == 64 ? 4 : 2, WT = 8 / WN;

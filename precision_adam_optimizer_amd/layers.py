@@ -167,8 +167,9 @@ class Packed8:
 
     codes: uint8 (of format ``fmt``) or a float8 tensor, [rows, cols rounded up to 128], with zeros
     behind ``cols``; rows may lie further apart, by a multiple of 16.  scales: [rows, blocks], either
-    uint8 or float8_e8m0fnu bytes b that stand for 2^(b - 127), or float32 powers of two, as
-    ``Quantizer`` writes them.
+    uint8 or float8_e8m0fnu bytes b that stand for 2^(b - 127) (copied if their rows are not whole
+    dwords: multiples of 4 bytes, apart and in length), or float32 powers of two, as ``Quantizer``
+    writes them.  Scales lie between 2^-126 and 2^127.
     """
     __slots__ = ("_room", "_codes", "_scales", "rows", "cols", "format", "scale_type", "device", "_fields")
 
@@ -204,21 +205,33 @@ class Packed8:
     @classmethod
     def _new(cls, rows: int, cols: int, fmt: str, device) -> "Packed8":
         """Room for a matrix, codes and scales in one allocation."""
-        p = cls.__new__(cls)
-        blocks = -(-cols // BLOCK)
+        return cls._several(1, rows, cols, fmt, device)[0]
+
+    @classmethod
+    def _several(cls, n: int, rows: int, cols: int, fmt: str, device) -> list:
+        """Room for n matrices in one allocation, which lives as long as one of them: an allocation takes a
+        small call 3 us."""
+        blocks, fmt8 = -(-cols // BLOCK), _FORMATS[fmt]
         ld, ld_scale = BLOCK * blocks, -(-blocks // 4) * 4
-        p._room = torch.empty(rows * (ld + ld_scale), dtype=torch.uint8, device=device)
-        p._codes = None
-        p.rows, p.cols, p.format, p.scale_type, p.device = rows, cols, _FORMATS[fmt], SCALES_E8M0, device
-        at = p._room.data_ptr()
-        p._fields = (at, at + rows * ld, ld, ld_scale, p.format, SCALES_E8M0)
-        return p
+        size = -(-rows * (ld + ld_scale) // 256) * 256
+        room = torch.empty(n * size, dtype=torch.uint8, device=device)
+        first = room.data_ptr()
+        made = []
+        for i in range(n):
+            p = cls.__new__(cls)
+            p._room, p._codes = room, None
+            p.rows, p.cols, p.format, p.scale_type, p.device = rows, cols, fmt8, SCALES_E8M0, device
+            at = first + i * size
+            p._fields = (at, at + rows * ld, ld, ld_scale, fmt8, SCALES_E8M0)
+            made.append(p)
+        return made
 
     def _views(self):
         if self._codes is None:
-            ld, ld_scale = self._fields[2:4]
-            self._codes = self._room.as_strided((self.rows, ld), (ld, 1))
-            self._scales = self._room.as_strided((self.rows, ld_scale), (ld_scale, 1), self.rows * ld)
+            at, _, ld, ld_scale = self._fields[:4]
+            at -= self._room.data_ptr()
+            self._codes = self._room.as_strided((self.rows, ld), (ld, 1), at)
+            self._scales = self._room.as_strided((self.rows, ld_scale), (ld_scale, 1), at + self.rows * ld)
         return self._codes, self._scales
 
     @property
@@ -402,8 +415,9 @@ def _product(x, w: Packed8, w_up, bias, act: str, residual, dtype, fmt: str, kee
     else:
         y = _NO_MATRIX
     y8 = None if pack is None else Packed8._new(T, N, pack, device)
-    z = None if keep is None else Packed8._new(T, N, keep, device)
-    z_up = Packed8._new(T, N, keep, device) if gated and keep is not None else None
+    z = z_up = None
+    if keep is not None:
+        z, z_up = Packed8._several(2, T, N, keep, device) if gated else (Packed8._new(T, N, keep, device), None)
     args = _PRODUCT8.pack(
         T, N, K, *x_in, *x8._fields, *w._fields, *(_is8(w_up, "w_up", N, K, device)._fields if gated else _NO_MATRIX8),
         *(_NO_MATRIX if bias is None else _vector(bias, "bias", N, device)),
