@@ -623,7 +623,8 @@ auto guarded(const char* what, F&& body) -> decltype(body()) {
 // within 15% of what was measured, and their order right: 2048 x 2048 x 2048 as 128 x 128 in one
 // part 45 estimated 38, as 256 x 256 in four parts 51 estimated 53; 2048 tokens x 2 pairs of 2048 x 768
 // as 128 x 128 in five parts 35 estimated 40, as 256 x 256 in eight 40 estimated 46; 16384 tokens
-// x 2048 x 768 as 256 x 256 in ten parts 80 estimated 87, as 128 x 128 in five 88 estimated 93.)
+// x 2048 x 768 as 256 x 256 in ten parts 80 estimated 87, as 128 x 128 in five 88 estimated 93.)  Of large
+// numbers of parts one in eight is looked at: all 768 of a single tile would take the host longer than the kernel's launch.
 GradPlan plan_grad(int64_t m, int64_t k, int64_t r, int npairs) {
   const int64_t steps = (r + 63) / 64 * npairs, ldp = (k + 3) & ~(int64_t)3;
   GradPlan best{0, 1, 0};
@@ -632,7 +633,7 @@ GradPlan plan_grad(int64_t m, int64_t k, int64_t r, int npairs) {
     const int64_t size = tile ? 128 : 256, slots = tile ? 512 : 256;
     const int64_t tiles = std::max<int64_t>(1, (m + size - 1) / size * ((k + size - 1) / size));
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(slots / tiles, steps / 2));
-    for (int64_t splits = 1; splits <= most; splits++) {
+    for (int64_t splits = 1;; splits = std::min(most, splits + std::max<int64_t>(1, splits / 8))) {
       const int64_t groups = tiles * splits;
       const double step = tile ? (groups > 256 ? 1.35 : 1.0) : 2.0;
       double t = (double)((groups + slots - 1) / slots) * (double)((steps + splits - 1) / splits) * step;
@@ -641,6 +642,7 @@ GradPlan plan_grad(int64_t m, int64_t k, int64_t r, int npairs) {
         least = t;
         best = GradPlan{tile, (int)splits, splits > 1 ? splits * m * ldp * (int64_t)sizeof(float) : 0};
       }
+      if (splits == most) break;
     }
   }
   return best;
