@@ -594,9 +594,23 @@ int launch_few(const ProductArgs& a, hipStream_t s) {
   return go(k_product_few<XF, WF, GATED, 4, kCodes, WAVES>);
 }
 
+// 17 to 64 tokens: whether tiles of 64 tokens, with codes widened, take less time than k_product_few, in us.  That
+// reads the weights at 4 TB/s and has every work-group of 16 rows read every token, at 7 TB/s from the caches; a tile takes
+// 0.88 for each block of 128 columns.  (4096 to 2 * 11008 with 17, 32 and 64 tokens: few 29, 35 and 54,
+// estimated 29, 35 and 48; tiles 33, estimated 33.  11008 to 4096 with 64: few 32, tiles, of which there are 16, 80 estimated.)
+inline bool tile_is_faster(const ProductArgs& a, bool gated) {
+  const double nk = (a.cols + 127) >> 7, weights = (gated ? 256.0 : 128.0) * nk * a.rows;
+  const double few = weights / 4e6 + 128.0 * nk * (double)a.tokens * (double)((a.rows + 15) / 16) / 7e6;
+  const int64_t tiles = (a.rows + (gated ? 127 : 255)) / (gated ? 128 : 256);
+  return 5.0 + 0.88 * nk * (double)((tiles + 255) / 256) < few;
+}
+
 template <int XF, int WF, bool GATED>
 int launch_product_of(const ProductArgs& a, hipStream_t s) {
-  if (few_tokens(a)) return a.rows >= 16 * 512 ? launch_few<XF, WF, GATED, 4>(a, s) : launch_few<XF, WF, GATED, 8>(a, s);
+  if (few_tokens(a)) {
+    if (a.tokens > 16 && tile_is_faster(a, GATED)) return launch_tiles<XF, WF, GATED, 64, true>(a, s);
+    return a.rows >= 16 * 512 ? launch_few<XF, WF, GATED, 4>(a, s) : launch_few<XF, WF, GATED, 8>(a, s);
+  }
   if (a.y && a.y_dt == FP8ADAM_F32) return launch_tiles<XF, WF, GATED, 128, true>(a, s);
   // the tile whose rounds over 256 CUs cost least: a tile of 128 and of 64 tokens takes about 0.68 and
   // 0.45 of the time of one of 256 (2048 x 8192 x 2048, in one, two and four rounds: 34, 44, 59 us)

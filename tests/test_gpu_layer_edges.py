@@ -138,6 +138,28 @@ def test_sums_in_many_parts(tokens, rows, cols, n):
     close(out, want, rounded(t + 2.0 ** -23 * want.abs(), want, F16))
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("tokens", [17, 50, 64])
+def test_some_tokens_of_wide_layers(tokens, fmt):
+    """17 to 64 tokens of layers with so many outputs that the tiled product takes them: sums as exact as those of few tokens."""
+    cols, rows = 1100, 40003
+    for n, (dtype, kind) in enumerate([(F32, "none"), (BF16, "relu"), (F16, "relu")]):
+        x = u.randn((tokens, cols), n, dtype=dtype, spread=1.0)
+        w = pk.pack8(u.randn((rows, cols), 4 + n) / cols ** 0.5, fmt)
+        b, r = u.randn((rows,), 7, dtype=F16), u.randn((tokens, rows), 8, dtype=BF16)
+        got = pk.linear8(x, w, bias=b, activation=kind, residual=r, dtype=dtype)
+        xv, wv = u.values(got.x), u.values(w)
+        extra = b.double().abs() + r.double().abs()
+        y, t = u.act(xv @ wv.t() + b.double(), kind) + r.double(), u.sum_bound(xv.abs() @ wv.abs().t() + extra, cols + 3)
+        close(got.y, y, rounded(t, y, dtype))
+        half = pk.Packed8(w.codes[:20001], w.scales[:20001], cols, fmt)
+        other = pk.Packed8(w.codes[20001:40002], w.scales[20001:40002], cols, fmt)
+        got = pk.gated8(x, half, other, activation="none", dtype=dtype)
+        g, up = xv @ wv[:20001].t(), xv @ wv[20001:40002].t()
+        tg, tu = (u.sum_bound(xv.abs() @ v.abs().t(), cols + 2) for v in (wv[:20001], wv[20001:40002]))
+        close(got.y, g * up, rounded(tg * (up.abs() + tu) + tu * g.abs() + 2.0 ** -23 * (g * up).abs(), g * up, dtype))
+
+
 def test_on_another_stream_than_the_tensors_own():
     """Tensors made on one stream, calls on another that waits for it, results read on the first again."""
     w = pk.pack8(u.randn((384, 256), 1) / 16)
