@@ -167,9 +167,12 @@ class Packed8:
 
     codes: uint8 (of format ``fmt``) or a float8 tensor, [rows, cols rounded up to 128], with zeros
     behind ``cols``; rows may lie further apart, by a multiple of 16.  scales: [rows, blocks], either
-    uint8 or float8_e8m0fnu bytes b that stand for 2^(b - 127) (copied if their rows are not whole
-    dwords: multiples of 4 bytes, apart and in length), or float32 powers of two, as ``Quantizer``
+    uint8 or float8_e8m0fnu bytes b that stand for 2^(b - 127), or float32 powers of two, as ``Quantizer``
     writes them.  Scales lie between 2^-126 and 2^127.
+
+    Codes and scales are views: what is written to them later is what later calls read.  Only where rows of
+    bytes are not whole dwords (multiples of 4 bytes, apart and in length, from an address that is one) are
+    both copied, and the matrix stays as it was when it was made.
     """
     __slots__ = ("_room", "_codes", "_scales", "rows", "cols", "format", "scale_type", "device", "_fields")
 
@@ -193,10 +196,11 @@ class Packed8:
         self.scale_type = SCALES_F32 if scales.dtype == torch.float32 else SCALES_E8M0
         if self.scale_type == SCALES_E8M0 and (scales.shape[1] % 4 or (scales.stride(0) % 4 and self.rows > 1) or
                                                 scales.data_ptr() % 4 or scales.stride(1) != 1):
-            # whole dwords per row, as the kernels read them
+            # whole dwords per row, as the kernels read them; the codes with them, or codes rewritten later would be
+            # multiplied by scales of before
             padded = scales.new_full((self.rows, -(-blocks // 4) * 4), 127)
             padded[:, :blocks] = scales[:, :blocks]
-            scales = padded
+            codes, scales = codes.clone(memory_format=torch.contiguous_format), padded
         self._codes, self._scales, self.device = codes, scales, codes.device
         many = self.rows > 1
         self._fields = (codes.data_ptr(), scales.data_ptr(), codes.stride(0) if many else codes.shape[1],

@@ -1,0 +1,49 @@
+"""The layer operators' binding, without a GPU: what a Packed8 holds of the tensors that it was made of."""
+import pytest
+import torch
+
+import precision_adam_optimizer_amd as pk
+
+U8 = torch.uint8
+
+
+def made(rows, cols, scales):
+    """(codes, scales, Packed8) whose values are all 1."""
+    nb = -(-cols // 128)
+    codes = torch.full((rows, 128 * nb), 0x38, dtype=U8)  # 1.0 in E4M3
+    return codes, scales, pk.Packed8(codes, scales, cols)
+
+
+def values(p):
+    c, s = p.values()
+    if p.scale_type == 0:
+        s = torch.exp2(s.view(U8).float() - 127)
+    return c.float() * s.repeat_interleave(128, 1)[:, :p.cols]
+
+
+@pytest.mark.parametrize("make", [
+    lambda: torch.full((5, 6), 127, dtype=U8),                       # six blocks: not whole dwords
+    lambda: torch.full((5, 6), 127, dtype=U8).view(torch.float8_e8m0fnu),
+    lambda: torch.full((5, 11), 127, dtype=U8)[:, 2:8],              # rows 11 bytes apart, off a dword
+    lambda: torch.full((5, 8), 127, dtype=U8)[:, :6],                # whole dwords apart, not as long
+    lambda: torch.full((41,), 127, dtype=U8)[1:].view(5, 8),         # whole dwords long, off a dword
+])
+def test_copied_scales_come_with_copied_codes(make):
+    """Scales whose rows are not whole dwords are copied.  Codes and scales rewritten in place later are
+    then seen together or not at all: never new codes with old scales."""
+    codes, scales, p = made(5, 768, make())
+    assert (values(p) == 1).all()
+    assert p.scales.data_ptr() != scales.data_ptr() and p.codes.data_ptr() != codes.data_ptr()
+    codes.fill_(0x40)  # 2.0
+    scales.view(U8).fill_(129)
+    assert (values(p) == 1).all()
+    assert p.arg()[:2] == (p.codes.data_ptr(), p.scales.data_ptr())
+
+
+@pytest.mark.parametrize("make", [lambda: torch.full((5, 8), 127, dtype=U8), lambda: torch.ones(5, 6), lambda: torch.ones(5, 9)[:, 1:7]])
+def test_other_scales_are_seen_with_their_codes(make):
+    codes, scales, p = made(5, 768, make())
+    assert p.scales.data_ptr() == scales.data_ptr() and p.codes.data_ptr() == codes.data_ptr()
+    codes.fill_(0x40)
+    scales.fill_(128 if scales.dtype == U8 else 2.0)
+    assert (values(p) == 4).all()
