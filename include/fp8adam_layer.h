@@ -78,7 +78,7 @@ int fp8adam_unpack8(const fp8adam_matrix8 *in, const fp8adam_matrix *x, int64_t 
  *   gated8:   g = x w^T, u = x w_up^T;  y = act(g) * u
  * in fp32 up to here; y is then rounded to its type (to nearest even), and y8 is y before that rounding in
  * 8 bits.  keep (z or g) and keep_up (u) are those sums in 8 bits.  Where y is fp32, and with up to 64
- * tokens and neither y8 nor keep, every product is exact and added in fp32.  Otherwise the FP8 matrix
+ * tokens, every product is exact and added in fp32 (in another order where something is kept).  Otherwise the FP8 matrix
  * instruction adds eight products of consecutive columns at a time, each cut at 2^-13 of the power of two of the
  * largest's exponents, and these sums in fp32: p is then off by up to 7 * 2^-13 of the sum of the largest
  * products of all eights (typically 1.4e-5 of p's rms), well below the roundings to 16 and 8 bits.  x_in: if given, x is written first

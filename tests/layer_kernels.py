@@ -38,16 +38,16 @@ def products():
         half = 2 if gated else 1  # a tile holds 256 rows of weights, or 128 of either projection
         for n, (tt, wide, tokens, rows, dtype) in enumerate([
                 (64, False, 700, 1300, "bf16"), (128, False, 2048, 2600, "bf16"), (256, False, 4100, 2600, "bf16"),
-                (64, True, 60, 120000, "bf16"), (128, True, 300, 1030, "fp32")]):
+                (64, True, 60, 120000, "bf16"), (64, True, 50, 1300, "fp16"), (128, True, 300, 1030, "fp32")]):
             call = Product(gated, tokens, rows // half, 0, dtype)
-            kept = not wide or dtype == "fp32"
-            for m, cols in enumerate([100, 640, 1000, 7300] if rows < 5000 else [1100, 1153]):
+            kept = rows < 5000  # (kept or packed with few tokens: the tile; neither: the tile only for many outputs)
+            for m, cols in enumerate([100, 640, 1000, 7300] if kept else [1100, 1153]):
                 got.append((tt, wide, call._replace(
-                    cols=cols, keep=kept and m % 2 == 0, pack="e5m2" if kept and m == 1 else None, packed=m == 2,
+                    cols=cols, keep=kept and m != 1, pack="e5m2" if kept and m == 1 else None, packed=m == 2,
                     dtype="fp16" if dtype == "bf16" and m % 2 else dtype, activation=("none", "silu", "gelu", "relu")[(m + n) % 4],
                     bias=not gated and m < 2, residual=not gated and m > 0)))
             for x, w in (("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")):
-                got.append((tt, wide, call._replace(cols=1153 if rows > 5000 else 900, x=x, w=w, keep=kept)))
+                got.append((tt, wide, call._replace(cols=900 if kept else 1153, x=x, w=w, keep=kept)))
     return got
 
 
