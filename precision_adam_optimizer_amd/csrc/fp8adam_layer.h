@@ -336,6 +336,7 @@ struct ProductArgs {
   Out8 y8, keep[2];
   int32_t act, xin_dt, bias_dt, res_dt, y_dt;
   int32_t tiles_n, tiles_t;
+  int32_t exact;             // host: every product is added in 32 bits, whatever is written
 };
 
 // The kernel for few tokens, which keeps nothing in 8 bits (a block of 128 outputs spans its

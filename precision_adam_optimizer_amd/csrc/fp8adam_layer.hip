@@ -340,6 +340,7 @@ int product8(const fp8adam_product8* p, bool gated, hipStream_t s) {
   const int64_t T = p->tokens, N = p->rows, K = p->cols;
   if (int r = check_sizes(T, N, K)) return r;
   if (!valid_act(p->activation)) return fail(FP8ADAM_EINVAL, "bad activation");
+  if (p->exact != 0 && p->exact != 1) return fail(FP8ADAM_EINVAL, "exact must be 0 or 1");
   Memory mem;
   const bool packs = p->x_in.data != nullptr;
   if (packs)
@@ -393,6 +394,7 @@ int product8(const fp8adam_product8* p, bool gated, hipStream_t s) {
   if (p->keep.codes) a.keep[0] = out8(p->keep);
   if (p->keep_up.codes) a.keep[1] = out8(p->keep_up);
   a.act = p->activation;
+  a.exact = p->exact;
   if (packs) {
     if (packs_itself(a, p->x_in)) {
       a.xin = p->x_in.data;

@@ -48,7 +48,7 @@ class Product8Arg(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("x_in", MatrixArg),
                 ("x", Matrix8Arg), ("w", Matrix8Arg), ("w_up", Matrix8Arg), ("bias", MatrixArg), ("residual", MatrixArg),
                 ("y", MatrixArg), ("y8", Matrix8Arg), ("keep", Matrix8Arg), ("keep_up", Matrix8Arg),
-                ("activation", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                ("activation", ctypes.c_int32), ("exact", ctypes.c_int32)]
 
 
 class ActBackward8Arg(ctypes.Structure):
@@ -397,7 +397,7 @@ class Gated8(NamedTuple):
     y8: Packed8 | None
 
 
-def _product(x, w: Packed8, w_up, bias, act: str, residual, dtype, fmt: str, keep, pack, out):
+def _product(x, w: Packed8, w_up, bias, act: str, residual, dtype, fmt: str, keep, pack, out, exact: bool):
     gated = w_up is not None
     _need(isinstance(w, Packed8), "the weights must be a Packed8")
     N, K, device = w.rows, w.cols, w.device
@@ -427,31 +427,35 @@ def _product(x, w: Packed8, w_up, bias, act: str, residual, dtype, fmt: str, kee
         *(_NO_MATRIX if bias is None else _vector(bias, "bias", N, device)),
         *(_NO_MATRIX if residual is None else _arg(residual, "residual", T, N, device)), *y,
         *(_NO_MATRIX8 if y8 is None else y8._fields), *(_NO_MATRIX8 if z is None else z._fields),
-        *(_NO_MATRIX8 if z_up is None else z_up._fields), _act(act), 0)
+        *(_NO_MATRIX8 if z_up is None else z_up._fields), _act(act), 1 if exact else 0)
     _call_on("gated8" if gated else "linear8", args, device)
     return out, x8, z, z_up, y8
 
 
 def linear8(x, w: Packed8, *, bias=None, activation: str = "none", residual=None, dtype=torch.bfloat16, fmt: str = "e4m3",
-            keep: str | None = None, pack: str | None = None, out=None) -> Linear8:
+            keep: str | None = None, pack: str | None = None, out=None, exact: bool = False) -> Linear8:
     """activation(x w^T + bias) + residual, of x and w in 8 bits.
 
     x: [..., cols], packed in ``fmt`` by the same call, or a ``Packed8``.  w: [rows, cols].
     activation: "none", "relu", "silu" or "gelu" (with erf).  ``keep``: the format in which the sum
     before the activation is kept for ``linear8_backward``.  y goes to ``out`` (which may be the residual
     itself) or a new tensor of ``dtype`` (None: not written); ``pack``: the format in which it is
-    also written in 8 bits, for the next layer."""
-    y, x8, z, _, y8 = _product(x, w, None, bias, activation, residual, dtype, fmt, keep, pack, out)
+    also written in 8 bits, for the next layer.
+
+    More than 64 tokens without an fp32 y are summed by the FP8 matrix instruction, which cuts products far below the
+    largest of eight (the C header says by how much).  ``exact``: every product is added in fp32 there too, in up to
+    twice the time."""
+    y, x8, z, _, y8 = _product(x, w, None, bias, activation, residual, dtype, fmt, keep, pack, out, exact)
     return Linear8(y, x8, z, y8)
 
 
 def gated8(x, w_gate: Packed8, w_up: Packed8, *, activation: str = "silu", dtype=torch.bfloat16, fmt: str = "e4m3",
-           keep: str | None = None, pack: str | None = None, out=None) -> Gated8:
+           keep: str | None = None, pack: str | None = None, out=None, exact: bool = False) -> Gated8:
     """activation(x w_gate^T) * (x w_up^T): both projections, the activation and the product in one kernel.
 
     Arguments as for ``linear8``; ``keep`` keeps both projections for ``gated8_backward``."""
     _need(isinstance(w_up, Packed8), "the weights must be a Packed8")
-    y, x8, gate, up, y8 = _product(x, w_gate, w_up, None, activation, None, dtype, fmt, keep, pack, out)
+    y, x8, gate, up, y8 = _product(x, w_gate, w_up, None, activation, None, dtype, fmt, keep, pack, out, exact)
     return Gated8(y, x8, gate, up, y8)
 
 

@@ -18,6 +18,7 @@ class Product(NamedTuple):
     activation: str = "none"
     bias: bool = False
     residual: bool = False
+    exact: bool = False
 
 
 class Grad(NamedTuple):
@@ -48,6 +49,9 @@ def products():
                     bias=not gated and m < 2, residual=not gated and m > 0)))
             for x, w in (("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")):
                 got.append((tt, wide, call._replace(cols=900 if kept else 1153, x=x, w=w, keep=kept)))
+        for n, cols in enumerate((900, 7300)):  # 8 and 16 bits of every product
+            call = Product(gated, 700, 1300 // half, cols, ("bf16", "fp16")[n], True, ("e4m3", None)[n], activation="silu", exact=True)
+            got += [(128, True, call), (64, True, call._replace(tokens=50))]
     return got
 
 

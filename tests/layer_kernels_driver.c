@@ -48,12 +48,12 @@ int main(void) {
     while (scanf("%15s %ld %ld %ld", op, &T, &N, &K) == 4) {
         int rc;
         if (!strcmp(op, "linear8") || !strcmp(op, "gated8")) {
-            int xf, wf, x_dt, y_dt, keep, pack; /* x_dt, y_dt, pack: -1 is absent */
-            if (scanf("%d %d %d %d %d %d", &xf, &wf, &x_dt, &y_dt, &keep, &pack) != 6) return 2;
+            int xf, wf, x_dt, y_dt, keep, pack, exact; /* x_dt, y_dt, pack: -1 is absent */
+            if (scanf("%d %d %d %d %d %d %d", &xf, &wf, &x_dt, &y_dt, &keep, &pack, &exact) != 7) return 2;
             const int gated = op[0] == 'g';
             fp8adam_product8 p;
             memset(&p, 0, sizeof p);
-            p.tokens = T, p.rows = N, p.cols = K, p.activation = FP8ADAM_ACT_SILU;
+            p.tokens = T, p.rows = N, p.cols = K, p.activation = FP8ADAM_ACT_SILU, p.exact = exact;
             p.x = mat8(1, K, xf), p.w = mat8(2, K, wf);
             if (x_dt >= 0) p.x_in = mat(0, K, x_dt);
             if (gated) p.w_up = mat8(3, K, wf);

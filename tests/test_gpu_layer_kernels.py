@@ -29,7 +29,7 @@ def check_product(c, eights):
     xv = u.decode(codes, scales, c.cols, c.x)
     w, wv = weights(c.rows, c.cols, 2, c.w)
     src = pk.pack8(x, c.x) if c.packed else x
-    kw = dict(activation=c.activation, dtype=dtype, fmt=c.x, keep="e4m3" if c.keep else None, pack=c.pack)
+    kw = dict(activation=c.activation, dtype=dtype, fmt=c.x, keep="e4m3" if c.keep else None, pack=c.pack, exact=c.exact)
     z = xv @ wv.t()
     if c.gated:
         w_up, wv_up = weights(c.rows, c.cols, 3, c.w)

@@ -47,3 +47,13 @@ def test_few_tokens_keep_small_products(tokens, dtype, gated):
     for kw in ({}, dict(keep="e4m3"), dict(pack="e5m2"), dict(keep="e5m2", pack="e4m3")):
         for name, v in outputs(gated, tokens, 130, dtype, **kw).items():
             assert (v == EXACT).all(), (name, kw)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("tokens", [3, 65, 300])
+def test_exact_keeps_small_products(tokens, dtype, gated):
+    """Of any number of tokens, whatever is written."""
+    for kw in ({}, dict(keep="e4m3"), dict(pack="e5m2"), dict(keep="e5m2", pack="e4m3")):
+        for name, v in outputs(gated, tokens, 130, dtype, exact=True, **kw).items():
+            assert (v == EXACT).all(), (name, kw)

@@ -1,8 +1,11 @@
-"""The layer operators' binding, without a GPU: what a Packed8 holds of the tensors that it was made of."""
+"""The layer operators' binding, without a GPU: what a Packed8 holds of the tensors that it was made of, and refusals."""
+import ctypes
+
 import pytest
 import torch
 
 import precision_adam_optimizer_amd as pk
+from precision_adam_optimizer_amd import layers
 
 U8 = torch.uint8
 
@@ -47,3 +50,11 @@ def test_other_scales_are_seen_with_their_codes(make):
     codes.fill_(0x40)
     scales.fill_(128 if scales.dtype == U8 else 2.0)
     assert (values(p) == 4).all()
+
+
+def test_exact_is_a_truth_value():
+    for fn in ("fp8adam_linear8", "fp8adam_gated8"):
+        for exact in (-1, 2):
+            args = layers.Product8Arg(tokens=1, rows=1, cols=1, exact=exact)
+            assert getattr(layers._lib(), fn)(ctypes.byref(args), None) == -1
+            assert "exact must be 0 or 1" in pk.fp8adam_last_error()

@@ -44,7 +44,7 @@ def kernel(mangled):
 
 def product_line(c):
     return (f"{'gated8' if c.gated else 'linear8'} {c.tokens} {c.rows} {c.cols} {FORMATS[c.x]} {FORMATS[c.w]} "
-            f"{-1 if c.packed else DTYPES[c.dtype]} {DTYPES[c.dtype]} {int(c.keep)} {-1 if c.pack is None else FORMATS[c.pack]}")
+            f"{-1 if c.packed else DTYPES[c.dtype]} {DTYPES[c.dtype]} {int(c.keep)} {-1 if c.pack is None else FORMATS[c.pack]} {int(c.exact)}")
 
 
 def test_forward_tiles(launches):
