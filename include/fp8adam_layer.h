@@ -127,9 +127,9 @@ int fp8adam_gated8_backward(const fp8adam_act_backward8 *args, hipStream_t strea
 /* Gradients of a layer's weights and of its input, from dy [tokens, rows]:
  *   weight_grad8:  out[n,k] (+)= sum over t of dy[t,n] x[t,k]            out [rows, cols], b[0] = x [tokens, cols]
  *   input_grad8:   out[t,k] (+)= sum over i < n, n of dy_i[t,n] w_i[n,k]  out [tokens, cols], b[i] = w_i [rows, cols]
- * The products are of dy as it is (bf16), or split into two bf16 parts (fp16, whose 11 bits they hold; fp32,
- * of which they hold 16 bits: each product is off by at most 2^-16 of its size), with the values that the
- * codes stand for, summed in fp32; out is rounded once (to nearest even). */
+ * The products are of dy as it is (bf16), or split into bf16 parts: two (fp16, whose 11 bits they hold), or of fp32
+ * three with `exact`, which hold its 24 bits, and two without, which hold 16 (each product is off by at most 2^-16 of its
+ * size).  They are taken with the values that the codes stand for and summed in fp32; out is rounded once (to nearest even). */
 typedef struct {
     int64_t tokens, rows, cols;
     int32_t n;            /* input_grad8: layers, 1 or 2 (of one dtype of dy, format and type of scales); weight_grad8: 1 */
@@ -139,6 +139,8 @@ typedef struct {
     fp8adam_matrix out;
     void *workspace;      /* 16-byte aligned, of at least the size that the functions below give; NULL if that is 0 */
     int64_t workspace_bytes;
+    int32_t exact;        /* 1: fp32 dy in all of its bits (0: in 16, two thirds of the products) */
+    int32_t reserved;     /* 0 */
 } fp8adam_grad8;
 
 int64_t fp8adam_weight_grad8_workspace(const fp8adam_grad8 *args); /* or a negative error code */

@@ -358,7 +358,7 @@ int launch_product(const ProductArgs& a, bool gated, hipStream_t s);
 
 // out[m][k] (+)= sum over pairs and r of A(m, r) B[r][k]: A in bf16, stored [r][m] (trans) or
 // [m][r], rows 16-byte aligned and whole multiples of 8 elements (zeros behind the last); B in 8 bits.
-constexpr int kMaxPairs = 4;
+constexpr int kMaxParts = 3, kMaxPairs = 2 * kMaxParts;  // of a gradient, and of two layers
 struct GradArgs {
   const uint16_t* a[kMaxPairs];
   int64_t lda;               // the same for all pairs

@@ -178,33 +178,39 @@ __global__ __launch_bounds__(kThreads) void k_bias_join(const float* partial, in
 // ----------------------------------------------------------- the gradients' left side
 
 // A gradient as the products take it: bf16 with rows padded to a multiple of 8 (zeros), and where
-// it has more bits than bf16 what the first part leaves, as a second.  The first part is cut, not
-// rounded, so that it never passes the largest number; a NaN or Inf has no second part.
-template <int DT>
+// it has more bits than bf16 what that part leaves, as a second (the 11 bits of fp16 in 8 + 3), and what these
+// leave, as a third (the 24 of fp32 in 8 + 8 + 8).  All but the last are cut, not rounded, so that they never pass the
+// largest number and what is left has the bits that follow; a NaN or Inf is in the first part alone.
+template <int DT, int PARTS>
 __global__ __launch_bounds__(kThreads) void k_split(const void* x, int64_t ld, int64_t rows, int cols, int64_t ldo,
-                                                    uint16_t* hi, uint16_t* lo) {
+                                                    uint16_t* out, int64_t part) {
   const int64_t groups = ldo >> 3, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= rows * groups) return;
   const int64_t row = i / groups, c = (i - row * groups) * 8;
   float v[8];
   ld8<DT>(x, row * ld + c, cols - c, v);
-  uint32_t h[4], l[4];
 #pragma unroll
-  for (int q = 0; q < 4; q++) {
-    uint32_t hb[2];
-    float rest[2];
+  for (int p = 0; p < PARTS; p++) {
+    uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 2; e++) {
-      const uint32_t b = __float_as_uint(v[2 * q + e]);
-      const bool odd = (b & 0x7F800000u) == 0x7F800000u;
-      hb[e] = odd ? f32_to_bf16_rne(v[2 * q + e]) : b >> 16;
-      rest[e] = odd ? 0.0f : v[2 * q + e] - __uint_as_float(b & 0xFFFF0000u);
+    for (int q = 0; q < 4; q++) {
+      if (p > 0 && p == PARTS - 1) {
+        w[q] = fp8adam_list::pack2<FP8ADAM_BF16>(v[2 * q], v[2 * q + 1]);
+        continue;
+      }
+      uint32_t h[2];
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        float& x = v[2 * q + e];
+        const uint32_t b = __float_as_uint(x);
+        const bool odd = (b & 0x7F800000u) == 0x7F800000u;
+        h[e] = odd ? f32_to_bf16_rne(x) : b >> 16;
+        x = odd ? 0.0f : x - __uint_as_float(b & 0xFFFF0000u);
+      }
+      w[q] = h[0] | h[1] << 16;
     }
-    h[q] = hb[0] | hb[1] << 16;
-    l[q] = fp8adam_list::pack2<FP8ADAM_BF16>(rest[0], rest[1]);
+    st_global<vu4>(out + p * part + row * ldo + c, vu4{w[0], w[1], w[2], w[3]});
   }
-  st_global<vu4>(hi + row * ldo + c, vu4{h[0], h[1], h[2], h[3]});
-  if (lo) st_global<vu4>(lo + row * ldo + c, vu4{l[0], l[1], l[2], l[3]});
 }
 
 // ------------------------------------------------------------------------ host side
@@ -490,18 +496,18 @@ int act_backward(const fp8adam_act_backward8* p, bool gated, hipStream_t s) {
 // ---- gradients of weights and inputs
 
 // dy goes into the product as it is where it is bf16 with rows of whole 16-byte pieces; otherwise through
-// k_split, in one part (bf16) or two.
+// k_split, in one part (bf16), two (fp16, and fp32 in 16 bits) or three (fp32 in all of its bits).
 struct Left {
   bool direct;
   int parts;
   int64_t ld, bytes;  // of one part
 };
 
-Left left_of(const fp8adam_matrix& dy, int64_t tokens, int64_t rows) {
+Left left_of(const fp8adam_matrix& dy, int64_t tokens, int64_t rows, bool exact) {
   Left l{};
   const int64_t ld = tokens > 1 ? dy.ld : rows;  // one row's is not used
   l.direct = dy.dtype == FP8ADAM_BF16 && rows % 8 == 0 && ld % 8 == 0 && ((uintptr_t)dy.data & 15u) == 0;
-  l.parts = dy.dtype == FP8ADAM_BF16 ? 1 : 2;
+  l.parts = dy.dtype == FP8ADAM_BF16 ? 1 : dy.dtype == FP8ADAM_F32 && exact ? kMaxParts : 2;
   l.ld = l.direct ? ld : (rows + 7) & ~(int64_t)7;
   l.bytes = l.direct ? 0 : (tokens * l.ld * 2 + 255) & ~(int64_t)255;
   return l;
@@ -517,13 +523,14 @@ struct GradCall {
 int grad_call(const fp8adam_grad8* p, bool weights, GradCall& c) {
   if (!p) return fail(FP8ADAM_EINVAL, "args is null");
   if (int r = check_sizes(p->tokens, p->rows, p->cols)) return r;
+  if (p->exact != 0 && p->exact != 1) return fail(FP8ADAM_EINVAL, "exact must be 0 or 1");
   if (p->n < 1 || p->n > (weights ? 1 : 2)) return fail(FP8ADAM_EINVAL, weights ? "n must be 1" : "n must be 1 or 2");
   for (int i = 0; i < p->n; i++)
     if (p->dy[i].dtype < FP8ADAM_F32 || p->dy[i].dtype > FP8ADAM_F16 || p->dy[i].dtype != p->dy[0].dtype)
       return fail(FP8ADAM_EINVAL, "bad dtype of dy, or more than one");
   c.direct = true;
   for (int i = 0; i < p->n; i++) {
-    c.left[i] = left_of(p->dy[i], p->tokens, p->rows);
+    c.left[i] = left_of(p->dy[i], p->tokens, p->rows, p->exact);
     c.direct = c.direct && c.left[i].direct && c.left[i].ld == c.left[0].ld;
   }
   c.bytes = 0;
@@ -531,7 +538,7 @@ int grad_call(const fp8adam_grad8* p, bool weights, GradCall& c) {
     for (int i = 0; i < p->n; i++) {
       fp8adam_matrix other = p->dy[i];
       other.data = reinterpret_cast<void*>(2);  // not 16-byte aligned: through k_split
-      c.left[i] = left_of(other, p->tokens, p->rows);
+      c.left[i] = left_of(other, p->tokens, p->rows, p->exact);
       c.bytes += c.left[i].parts * c.left[i].bytes;
     }
   const int pairs = p->n * c.left[0].parts;
@@ -546,12 +553,14 @@ int64_t grad_workspace(const fp8adam_grad8* p, bool weights) {
   return p->tokens > 0 ? c.bytes : 0;
 }
 
-int run_split(const fp8adam_matrix& dy, int64_t tokens, int64_t rows, const Left& l, uint16_t* hi, uint16_t* lo, hipStream_t s) {
+int run_split(const fp8adam_matrix& dy, int64_t tokens, int64_t rows, const Left& l, uint16_t* out, hipStream_t s) {
   const int64_t groups = (tokens * (l.ld >> 3) + kThreads - 1) / kThreads;
   if (int r = check_groups(groups)) return r;
-  auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)groups), dim3(kThreads), 0, s, dy.data, dy.ld, tokens, (int)rows, l.ld, hi, lo); };
-  if (dy.dtype == FP8ADAM_F32) return go(k_split<FP8ADAM_F32>);
-  return dy.dtype == FP8ADAM_BF16 ? go(k_split<FP8ADAM_BF16>) : go(k_split<FP8ADAM_F16>);
+  auto go = [&](auto kernel) {
+    return launch(kernel, dim3((unsigned)groups), dim3(kThreads), 0, s, dy.data, dy.ld, tokens, (int)rows, l.ld, out, l.bytes / 2);
+  };
+  if (dy.dtype == FP8ADAM_F32) return l.parts == 3 ? go(k_split<FP8ADAM_F32, 3>) : go(k_split<FP8ADAM_F32, 2>);
+  return dy.dtype == FP8ADAM_BF16 ? go(k_split<FP8ADAM_BF16, 1>) : go(k_split<FP8ADAM_F16, 2>);
 }
 
 int grad8(const fp8adam_grad8* p, bool weights, hipStream_t s) {
@@ -582,13 +591,11 @@ int grad8(const fp8adam_grad8* p, bool weights, hipStream_t s) {
   for (int i = 0; i < p->n; i++) {
     const Left& l = c.left[i];
     for (int q = 0; q < l.parts; q++) {
-      a.a[a.npairs] = c.direct ? static_cast<const uint16_t*>(p->dy[i].data) : reinterpret_cast<const uint16_t*>(ws + q * l.bytes);
+      a.a[a.npairs] = static_cast<const uint16_t*>(c.direct ? p->dy[i].data : ws + q * l.bytes);
       a.b[a.npairs++] = in8(p->b[i]);
     }
     if (!c.direct && T > 0) {
-      uint16_t* hi = reinterpret_cast<uint16_t*>(ws);
-      uint16_t* lo = l.parts == 2 ? reinterpret_cast<uint16_t*>(ws + l.bytes) : nullptr;
-      if (int r = run_split(p->dy[i], T, N, l, hi, lo, s)) return r;
+      if (int r = run_split(p->dy[i], T, N, l, reinterpret_cast<uint16_t*>(ws), s)) return r;
       ws += l.parts * l.bytes;
     }
   }

@@ -134,7 +134,8 @@ __global__ __launch_bounds__(128 * WK, 2) void k_grad(const GradArgs a, int spli
   const int nb = (int)(((int64_t)a.k + 127) >> 7);
   const bool f32 = a.b[0].f32;
 
-  // The next block to load, of either half of A and of B: where it lies, and where it stands in the sum.
+  // The next block to load, of either half of A and of B: where it lies, and where it stands in the sum.  (The step from
+  // one pair to the next is kept out of the loop: between its loads the large products take 1 to 2% longer.)
   struct CursorA {
     const uint16_t* p;  // transposed: the block's first row; otherwise its first column
     int64_t r;
@@ -149,10 +150,10 @@ __global__ __launch_bounds__(128 * WK, 2) void k_grad(const GradArgs a, int spli
   const int esize = f32 ? 4 : 1;
   const int64_t a_step = TRANS ? kStep * a.lda : kStep, a_first = TRANS ? m0 : m0 * a.lda;
   auto a_of = [&](int pair, int64_t r) {
-    return CursorA{(pair == 0 ? a.a[0] : pair == 1 ? a.a[1] : pair == 2 ? a.a[2] : a.a[3]) + a_first + r / kStep * a_step, r, pair};
+    return CursorA{(pair == 0 ? a.a[0] : pair == 1 ? a.a[1] : pair == 2 ? a.a[2] : pair == 3 ? a.a[3] : pair == 4 ? a.a[4] : a.a[5]) + a_first + r / kStep * a_step, r, pair};
   };
   auto b_of = [&](int pair, int64_t r) {
-    const In8& m = pair == 0 ? a.b[0] : pair == 1 ? a.b[1] : pair == 2 ? a.b[2] : a.b[3];
+    const In8& m = pair == 0 ? a.b[0] : pair == 1 ? a.b[1] : pair == 2 ? a.b[2] : pair == 3 ? a.b[3] : pair == 4 ? a.b[4] : a.b[5];
     return CursorB{m.codes + r * m.ld, static_cast<const uint8_t*>(m.scales) + r * m.ld_scale * esize, m.ld, m.ld_scale, r, pair};
   };
   // Behind the last pair nothing is there: resources of no bytes, zeros.
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(128 * WK, 2) void k_grad(const GradArgs a, int spli
       load_lds(r, lds + (2 * place + part) * kA + (wave + kWaves * i) * 1024, TRANS || c.r + ca[i] < a.r ? oa[part][i] : 0x7FFFFF00u, 0);
     c.r += kStep;
     c.p += a_step;
-    if (c.r >= a.r) c = a_of(c.pair + 1, 0);
+    if (__builtin_expect(c.r >= a.r, 0)) c = a_of(c.pair + 1, 0);
   };
   auto load_b = [&](int place, CursorB& c) __attribute__((always_inline)) {
     const int64_t rows = c.pair < a.npairs ? min((int64_t)kStep, a.r - c.r) : 0;
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(128 * WK, 2) void k_grad(const GradArgs a, int spli
     c.r += kStep;
     c.codes += kStep * c.ld;
     c.scales += kStep * c.ld_scale * esize;
-    if (c.r >= a.r) c = b_of(c.pair + 1, 0);
+    if (__builtin_expect(c.r >= a.r, 0)) c = b_of(c.pair + 1, 0);
   };
   auto widen_b = [&](int place) __attribute__((always_inline)) {
 #pragma unroll

@@ -61,14 +61,14 @@ class ActBackward8Arg(ctypes.Structure):
 class Grad8Arg(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("n", ctypes.c_int32),
                 ("accumulate", ctypes.c_int32), ("dy", MatrixArg * 2), ("b", Matrix8Arg * 2), ("out", MatrixArg),
-                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64), ("exact", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 # The same structs packed by the calls below: filling nested ctypes structures costs a small call 5 us.
 _M, _M8 = "Qqii", "QQqqii"
 _PRODUCT8 = Struct("@3q" + _M + 3 * _M8 + 3 * _M + 3 * _M8 + "2i")
 _ACT_BACKWARD8 = Struct("@2q" + _M + 2 * _M8 + 3 * _M + "Qq2i")
-_GRAD8 = Struct("@3q2i" + 2 * _M + 2 * _M8 + _M + "Qq")
+_GRAD8 = Struct("@3q2i" + 2 * _M + 2 * _M8 + _M + "Qq2i")
 
 _ready = None
 _calls: dict = {}  # the functions on packed structs, by name
@@ -505,19 +505,20 @@ def _with_room(name: str, struct: Struct, before: tuple, after: tuple, device: t
     _call_on(name, args, device)
 
 
-def _grad(name: str, dys, bs, out, T: int, N: int, K: int, rows: int, accumulate: bool) -> torch.Tensor:
+def _grad(name: str, dys, bs, out, T: int, N: int, K: int, rows: int, accumulate: bool, exact: bool) -> torch.Tensor:
     device = bs[0].device
     two = len(dys) == 2
     before = (T, N, K, len(dys), int(accumulate), *_arg(dys[0], "dy", T, N, device), *(_arg(dys[1], "dy", T, N, device) if two else _NO_MATRIX),
               *bs[0]._fields, *(bs[1]._fields if two else _NO_MATRIX8), *_arg(out, "out", rows, K, device))
-    _with_room(name, _GRAD8, before, (), device)
+    _with_room(name, _GRAD8, before, (1 if exact else 0, 0), device)
     return out
 
 
 def weight_grad8(dy: torch.Tensor, x: Packed8, out: torch.Tensor | None = None, *, accumulate: bool = False,
-                 dtype=torch.float32) -> torch.Tensor:
+                 dtype=torch.float32, exact: bool = True) -> torch.Tensor:
     """The gradient of a layer's weights, dy^T x [rows, cols], from the kept input: written to ``out`` (or a new
-    tensor of ``dtype``), or added to what stands there with ``accumulate``."""
+    tensor of ``dtype``), or added to what stands there with ``accumulate``.  An fp32 dy takes part in all of its bits, or
+    without ``exact`` in 16 of them, in two thirds of the time."""
     _need(isinstance(x, Packed8), "x must be a Packed8")
     m = _matrix(dy, "dy")
     _need(m.shape[0] == x.rows, f"dy must have {x.rows} rows")
@@ -525,12 +526,14 @@ def weight_grad8(dy: torch.Tensor, x: Packed8, out: torch.Tensor | None = None, 
     if out is None:
         _need(not accumulate, "accumulate needs out")
         out = torch.empty((N, x.cols), dtype=dtype, device=x.device)
-    return _grad("weight_grad8", [m], [x], out, x.rows, N, x.cols, N, accumulate)
+    return _grad("weight_grad8", [m], [x], out, x.rows, N, x.cols, N, accumulate, exact)
 
 
-def input_grad8(dy, w, out: torch.Tensor | None = None, *, accumulate: bool = False, dtype=torch.bfloat16) -> torch.Tensor:
+def input_grad8(dy, w, out: torch.Tensor | None = None, *, accumulate: bool = False, dtype=torch.bfloat16,
+                exact: bool = True) -> torch.Tensor:
     """The gradient of a layer's input, dy w [..., cols]; of two layers with one input (a gated pair) their sum, from
-    two gradients and two weights.  Written to ``out`` (or a new tensor of ``dtype``), or added to what stands there."""
+    two gradients and two weights.  Written to ``out`` (or a new tensor of ``dtype``), or added to what stands there.
+    ``exact`` as for ``weight_grad8``."""
     dys, ws = (list(dy), list(w)) if isinstance(dy, (list, tuple)) else ([dy], [w])
     _need(len(dys) == len(ws) and len(dys) in (1, 2), "need one gradient per layer, of one or two layers")
     _need(all(isinstance(p, Packed8) for p in ws), "the weights must be a Packed8")
@@ -544,4 +547,4 @@ def input_grad8(dy, w, out: torch.Tensor | None = None, *, accumulate: bool = Fa
     if out is None:
         _need(not accumulate, "accumulate needs out")
         out = torch.empty((*dys[0].shape[:-1], K), dtype=dtype, device=device)
-    return _grad("input_grad8", ms, ws, out, T, N, K, T, accumulate)
+    return _grad("input_grad8", ms, ws, out, T, N, K, T, accumulate, exact)

@@ -22,13 +22,15 @@ class Product(NamedTuple):
 
 
 class Grad(NamedTuple):
-    """A call of weight_grad8 (n = 0) or of input_grad8 for n layers."""
+    """A call of weight_grad8 (n = 0) or of input_grad8 for n layers.  fp32 gradients take part in three terms each, or
+    without `exact` in two, fp16 ones in two."""
     n: int
     tokens: int
     rows: int
     cols: int
     dtype: str = "bf16"
     fmt: str = "e4m3"
+    exact: bool = True
 
 
 def products():
@@ -73,7 +75,7 @@ def few():
 
 
 def gradients():
-    """(rows of a tile, whether the sum is in parts, call): odd and even numbers of steps of 64, one to four pairs
+    """(rows of a tile, whether the sum is in parts, call): odd and even numbers of steps of 64, one to six pairs
     of matrices, rows of dy that are whole 16-byte pieces and others."""
     got = []
     for fmt in ("e4m3", "e5m2"):
@@ -81,11 +83,13 @@ def gradients():
             got.append((256, False, Grad(0, tokens, 3304, 3300, "bf16", fmt)))
         got += [(256, False, Grad(0, 200, 3301, 3300, "bf16", fmt)), (256, False, Grad(0, 130, 3301, 3309, "fp32", fmt)),
                 (256, True, Grad(0, 4000, 2704, 900, "bf16", fmt)), (256, True, Grad(0, 4003, 2701, 897, "bf16", fmt)),
-                (256, True, Grad(0, 2000, 2704, 900, "fp16", fmt))]
+                (256, True, Grad(0, 2000, 2704, 900, "fp16", fmt)), (256, True, Grad(0, 1003, 2701, 900, "fp32", fmt)),
+                (256, True, Grad(0, 2000, 2701, 900, "fp32", fmt, False))]
         for rows in (8, 64, 72, 192, 257):
             for n in (1, 2):
                 got.append((256, False, Grad(n, 3301, rows, 3300, "bf16", fmt)))
         got += [(256, False, Grad(2, 3300, 130, 3301, "fp32", fmt)), (256, True, Grad(1, 2701, 4000, 900, "bf16", fmt)),
                 (256, True, Grad(2, 2703, 2001, 897, "bf16", fmt)), (256, True, Grad(2, 2700, 1000, 900, "fp16", fmt)),
+                (256, True, Grad(2, 2700, 500, 900, "fp32", fmt)), (256, True, Grad(2, 2701, 1000, 900, "fp32", fmt, False)),
                 (128, False, Grad(0, 700, 1024, 2304, "bf16", fmt)), (128, True, Grad(2, 129, 2000, 300, "fp32", fmt))]
     return got

@@ -63,12 +63,12 @@ int main(void) {
             if (keep && gated) p.keep_up = mat8(7, N, FP8ADAM_E4M3);
             rc = gated ? fp8adam_gated8(&p, NULL) : fp8adam_linear8(&p, NULL);
         } else {
-            int n, format, dy_dt;
-            if (scanf("%d %d %d", &n, &format, &dy_dt) != 3) return 2;
+            int n, format, dy_dt, exact;
+            if (scanf("%d %d %d %d", &n, &format, &dy_dt, &exact) != 4) return 2;
             const int weights = !strcmp(op, "weight_grad8");
             fp8adam_grad8 g;
             memset(&g, 0, sizeof g);
-            g.tokens = T, g.rows = N, g.cols = K, g.n = n, g.out = mat(4, K, FP8ADAM_F32), g.workspace = at(5);
+            g.tokens = T, g.rows = N, g.cols = K, g.n = n, g.out = mat(4, K, FP8ADAM_F32), g.workspace = at(5), g.exact = exact;
             for (int i = 0; i < n; i++) g.dy[i] = mat(i, N, dy_dt), g.b[i] = mat8(2 + i, K, format);
             g.workspace_bytes = weights ? fp8adam_weight_grad8_workspace(&g) : fp8adam_input_grad8_workspace(&g);
             rc = weights ? fp8adam_weight_grad8(&g, NULL) : fp8adam_input_grad8(&g, NULL);

@@ -57,3 +57,38 @@ def test_exact_keeps_small_products(tokens, dtype, gated):
     for kw in ({}, dict(keep="e4m3"), dict(pack="e5m2"), dict(keep="e5m2", pack="e4m3")):
         for name, v in outputs(gated, tokens, 130, dtype, exact=True, **kw).items():
             assert (v == EXACT).all(), (name, kw)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_gradients_take_every_bit_of_fp32(fmt):
+    """A number times 1, and what is left of two numbers that agree in their first 20 bits."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    # 24 random bits, from sizes whose last bit bf16 still holds as a normal number up to the largest
+    bits = torch.randint(0, 1 << 23, (1, 448), generator=g, device="cuda", dtype=torch.int32) | 1
+    dy = (bits | torch.arange(24, 24 + 448, device="cuda", dtype=torch.int32).clamp(max=254)[None] << 23).view(F32)
+    dy[:, ::3] *= -1
+    one = pk.pack8(torch.ones(1, 200, device="cuda"), fmt)
+    assert torch.equal(pk.weight_grad8(dy, one), dy.t().expand(448, 200))
+    for n in (1, 2):  # the first layer alone, and a second whose gradient is zero
+        ws = [pk.pack8(torch.eye(448, device="cuda"), fmt)] * n
+        dys = [dy, torch.zeros_like(dy)][:n]
+        assert torch.equal(pk.input_grad8(dys, ws, dtype=F32), dy)
+        assert torch.equal(pk.input_grad8(dys[::-1], ws, dtype=F32), dy)
+    near = torch.tensor([[1 + 2.0 ** -8 + 2.0 ** -20], [-1 - 2.0 ** -8]], device="cuda").expand(2, 200).contiguous()
+    ones = pk.pack8(torch.ones(2, 130, device="cuda"), fmt)
+    assert (pk.weight_grad8(near, ones) == 2.0 ** -20).all()
+    w = pk.pack8(torch.ones(200, 130, device="cuda"), fmt)
+    rest = near.clone()
+    rest[:, 1:] = 0
+    rest[:, 1] = -1 - 2.0 ** -8
+    assert (pk.input_grad8(rest[:1], w, dtype=F32) == 2.0 ** -20).all()
+    assert (pk.weight_grad8(near, ones, exact=False) == 0).all()  # 16 bits of each
+
+
+def test_gradients_of_one_token_are_rounded_once():
+    """One fp32 token: every element is one product, off by its rounding alone."""
+    dy = u.randn((1, 300), 1)
+    x = pk.pack8(u.randn((1, 500), 2))
+    want = dy.double().t() @ u.values(x)
+    assert ((pk.weight_grad8(dy, x).double() - want).abs() <= 3 * 2.0 ** -24 * want.abs()).all()  # three terms are added

@@ -58,3 +58,21 @@ def test_exact_is_a_truth_value():
             args = layers.Product8Arg(tokens=1, rows=1, cols=1, exact=exact)
             assert getattr(layers._lib(), fn)(ctypes.byref(args), None) == -1
             assert "exact must be 0 or 1" in pk.fp8adam_last_error()
+    for fn in ("fp8adam_weight_grad8", "fp8adam_input_grad8"):
+        for exact in (-1, 2):
+            args = layers.Grad8Arg(tokens=1, rows=1, cols=1, n=1, exact=exact)
+            assert getattr(layers._lib(), fn)(ctypes.byref(args), None) == -1
+            assert "exact must be 0 or 1" in pk.fp8adam_last_error()
+            assert getattr(layers._lib(), fn + "_workspace")(ctypes.byref(args)) == -1
+
+
+def test_workspace_of_fp32_gradients():
+    """Two bf16 parts of dy, and with `exact` three."""
+    for fn in ("fp8adam_weight_grad8_workspace", "fp8adam_input_grad8_workspace"):
+        for n in (1, 2) if "input" in fn else (1,):
+            size = []
+            for exact in (0, 1):
+                dy = layers.MatrixArg(data=1 << 32, ld=128, dtype=pk.F32)
+                args = layers.Grad8Arg(tokens=64, rows=128, cols=128, n=n, dy=(layers.MatrixArg * 2)(dy, dy), exact=exact)
+                size.append(getattr(layers._lib(), fn)(ctypes.byref(args)))
+            assert size[1] - size[0] >= n * 64 * 128 * 2

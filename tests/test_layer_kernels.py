@@ -72,7 +72,7 @@ def test_few_tokens(launches):
 def test_gradients(launches):
     cases = lk.gradients()
     reached = set()
-    lines = [f"{'input' if c.n else 'weight'}_grad8 {c.tokens} {c.rows} {c.cols} {c.n or 1} {FORMATS[c.fmt]} {DTYPES[c.dtype]}" for _, _, c in cases]
+    lines = [f"{'input' if c.n else 'weight'}_grad8 {c.tokens} {c.rows} {c.cols} {c.n or 1} {FORMATS[c.fmt]} {DTYPES[c.dtype]} {int(c.exact)}" for _, _, c in cases]
     for (tile, parts, c), got in zip(cases, launches(lines)):
         got = [k for k in got if k[0] != "k_split"]
         assert got[0] == ("k_grad", (int(not c.n), FORMATS[c.fmt], tile, tile, 4 if tile == 256 else 2)), c
