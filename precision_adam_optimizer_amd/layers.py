@@ -173,8 +173,11 @@ class Packed8:
     Codes and scales are views: what is written to them later is what later calls read.  Only where rows of
     bytes are not whole dwords (multiples of 4 bytes, apart and in length, from an address that is one) are
     both copied, and the matrix stays as it was when it was made.
+
+    A matrix that ``pack8`` or a product has made of a tensor of more dimensions stands for that tensor: a product
+    of it has the tensor's leading dimensions.
     """
-    __slots__ = ("_room", "_codes", "_scales", "rows", "cols", "format", "scale_type", "device", "_fields")
+    __slots__ = ("_room", "_codes", "_scales", "rows", "cols", "format", "scale_type", "device", "_fields", "_lead")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: str = "e4m3"):
         self.format = _FP8_FORMATS[codes.dtype] if codes.dtype in _FP8_FORMATS else _FORMATS[fmt]
@@ -201,18 +204,18 @@ class Packed8:
             padded = scales.new_full((self.rows, -(-blocks // 4) * 4), 127)
             padded[:, :blocks] = scales[:, :blocks]
             codes, scales = codes.clone(memory_format=torch.contiguous_format), padded
-        self._codes, self._scales, self.device = codes, scales, codes.device
+        self._codes, self._scales, self.device, self._lead = codes, scales, codes.device, (self.rows,)
         many = self.rows > 1
         self._fields = (codes.data_ptr(), scales.data_ptr(), codes.stride(0) if many else codes.shape[1],
                         scales.stride(0) if many else scales.shape[1], self.format, self.scale_type)
 
     @classmethod
-    def _new(cls, rows: int, cols: int, fmt: str, device) -> "Packed8":
-        """Room for a matrix, codes and scales in one allocation."""
-        return cls._several(1, rows, cols, fmt, device)[0]
+    def _new(cls, rows: int, cols: int, fmt: str, device, lead) -> "Packed8":
+        """Room for a matrix, codes and scales in one allocation; its rows stand for the dimensions ``lead``."""
+        return cls._several(1, rows, cols, fmt, device, lead)[0]
 
     @classmethod
-    def _several(cls, n: int, rows: int, cols: int, fmt: str, device) -> list:
+    def _several(cls, n: int, rows: int, cols: int, fmt: str, device, lead) -> list:
         """Room for n matrices in one allocation, which lives as long as one of them: an allocation takes a
         small call 3 us."""
         blocks, fmt8 = -(-cols // BLOCK), _FORMATS[fmt]
@@ -224,7 +227,7 @@ class Packed8:
         for i in range(n):
             p = cls.__new__(cls)
             p._room, p._codes = room, None
-            p.rows, p.cols, p.format, p.scale_type, p.device = rows, cols, fmt8, SCALES_E8M0, device
+            p.rows, p.cols, p.format, p.scale_type, p.device, p._lead = rows, cols, fmt8, SCALES_E8M0, device, lead
             at = first + i * size
             p._fields = (at, at + rows * ld, ld, ld_scale, fmt8, SCALES_E8M0)
             made.append(p)
@@ -362,7 +365,7 @@ def pack8(x: torch.Tensor, fmt: str = "e4m3") -> Packed8:
     """x in 8 bits, by rows of its last dimension: the operand of a product and the checkpoint of its input."""
     m = _matrix(x, "x")
     rows, cols = m.shape
-    out = Packed8._new(rows, cols, fmt, x.device)
+    out = Packed8._new(rows, cols, fmt, x.device, x.shape[:-1])
     a, b = MatrixArg(*_arg(m, "x", rows, cols, x.device)), Matrix8Arg(*out.arg())
     _run(lambda args, stream: _lib().fp8adam_pack8(*args, rows, cols, stream), (ctypes.byref(a), ctypes.byref(b)), x.device)
     return out
@@ -402,13 +405,13 @@ def _product(x, w: Packed8, w_up, bias, act: str, residual, dtype, fmt: str, kee
     _need(isinstance(w, Packed8), "the weights must be a Packed8")
     N, K, device = w.rows, w.cols, w.device
     if isinstance(x, Packed8):
-        T, lead = x.rows, (x.rows,)
+        T, lead = x.rows, x._lead
         x8, x_in = _is8(x, "x", T, K, device), _NO_MATRIX
     else:
         m = x if x.dim() == 2 else _matrix(x, "x")
         T, lead = m.shape[0], x.shape[:-1]
         x_in = _arg(m, "x", T, K, device)
-        x8 = Packed8._new(T, K, fmt, device)
+        x8 = Packed8._new(T, K, fmt, device, lead)
     _need(out is not None or dtype is not None or pack is not None, "nothing to write: dtype, out and pack are None")
     if out is not None:
         y = _arg(out, "out", T, N, device)
@@ -418,10 +421,10 @@ def _product(x, w: Packed8, w_up, bias, act: str, residual, dtype, fmt: str, kee
         y = (out.data_ptr(), N, _DTYPES[dtype], 0)
     else:
         y = _NO_MATRIX
-    y8 = None if pack is None else Packed8._new(T, N, pack, device)
+    y8 = None if pack is None else Packed8._new(T, N, pack, device, lead)
     z = z_up = None
     if keep is not None:
-        z, z_up = Packed8._several(2, T, N, keep, device) if gated else (Packed8._new(T, N, keep, device), None)
+        z, z_up = Packed8._several(2, T, N, keep, device, lead) if gated else (Packed8._new(T, N, keep, device, lead), None)
     args = _PRODUCT8.pack(
         T, N, K, *x_in, *x8._fields, *w._fields, *(_is8(w_up, "w_up", N, K, device)._fields if gated else _NO_MATRIX8),
         *(_NO_MATRIX if bias is None else _vector(bias, "bias", N, device)),
@@ -436,7 +439,7 @@ def linear8(x, w: Packed8, *, bias=None, activation: str = "none", residual=None
             keep: str | None = None, pack: str | None = None, out=None, exact: bool = False) -> Linear8:
     """activation(x w^T + bias) + residual, of x and w in 8 bits.
 
-    x: [..., cols], packed in ``fmt`` by the same call, or a ``Packed8``.  w: [rows, cols].
+    x: [..., cols], packed in ``fmt`` by the same call, or a ``Packed8`` of it.  w: [rows, cols].  y: [..., rows].
     activation: "none", "relu", "silu" or "gelu" (with erf).  ``keep``: the format in which the sum
     before the activation is kept for ``linear8_backward``.  y goes to ``out`` (which may be the residual
     itself) or a new tensor of ``dtype`` (None: not written); ``pack``: the format in which it is

@@ -76,3 +76,24 @@ def test_workspace_of_fp32_gradients():
                 args = layers.Grad8Arg(tokens=64, rows=128, cols=128, n=n, dy=(layers.MatrixArg * 2)(dy, dy), exact=exact)
                 size.append(getattr(layers._lib(), fn)(ctypes.byref(args)))
             assert size[1] - size[0] >= n * 64 * 128 * 2
+
+
+def test_packed_inputs_give_their_shape_to_the_output(monkeypatch):
+    """A matrix packed from a tensor of more dimensions, by pack8 or as a call's output or input, stands for that tensor:
+    what is made of it has the leading dimensions that it would have from the tensor itself."""
+    monkeypatch.setattr(layers, "_run", lambda *args: None)
+    w, w2 = (pk.Packed8(torch.zeros(r, 128 * -(-c // 128), dtype=U8), torch.full((r, 4), 127, dtype=U8), c) for r, c in ((24, 40), (40, 24)))
+    for lead in ((3, 5), (2, 3, 5), (15,), (0, 4), (2, 0, 4)):
+        x = torch.zeros(*lead, 40, dtype=torch.bfloat16)
+        for src in (x, pk.pack8(x)):
+            for r in (pk.linear8(src, w, keep="e4m3", pack="e4m3", activation="silu"), pk.gated8(src, w, w, keep="e4m3", pack="e5m2")):
+                assert r.y.shape == (*lead, 24)
+                assert pk.linear8(r.y8, w2, residual=x).y.shape == x.shape
+                assert pk.linear8(r.x, w, dtype=torch.float32).y.shape == (*lead, 24)
+                assert pk.gated8(r.x, w, w).y.shape == (*lead, 24)
+                for p in (r.x, r.y8):
+                    assert p.rows == x.numel() // 40
+                out = torch.zeros(p.rows, 24, dtype=torch.bfloat16)
+                assert pk.linear8(src, w, out=out).y is out
+    by_hand = pk.Packed8(torch.zeros(15, 128, dtype=U8), torch.full((15, 4), 127, dtype=U8), 40)
+    assert pk.linear8(by_hand, w).y.shape == (15, 24) and pk.unpack8(pk.pack8(torch.zeros(3, 5, 40))).shape == (15, 40)
