@@ -9,7 +9,8 @@ Activations and their gradients are matrices of fp32, bf16 or fp16, or tensors o
 whose leading ones fold into rows without a copy; a row is contiguous, rows may lie further apart.
 Calls go to the current stream of the tensors' device, allocate their results and workspaces with
 torch, wait for nothing, and may be captured into a graph.  Nothing is recorded by autograd: a
-backward pass calls the functions that end in ``_backward`` or ``_grad8`` itself.
+backward pass calls the functions that end in ``_backward`` or ``_grad8`` itself, and tensors that require a
+gradient are refused where autograd records (under ``torch.no_grad()`` and inside a ``torch.autograd.Function`` it does not).
 """
 from __future__ import annotations
 
@@ -295,8 +296,15 @@ def _matrix(t: torch.Tensor, what: str) -> torch.Tensor:
         raise ValueError(f"the leading dimensions of {what} do not fold into rows without a copy") from None
 
 
+def _recorded(what: str) -> None:
+    if torch.is_grad_enabled():
+        raise ValueError(f"{what} requires a gradient, which these calls do not record: call them under torch.no_grad() or detach it")
+
+
 def _arg(t: torch.Tensor, what: str, rows: int, cols: int, device) -> tuple:
     """The fields of the C struct of a matrix [rows, cols]."""
+    if t.requires_grad:
+        _recorded(what)
     if t.dim() != 2:
         t = _matrix(t, what)
     dtype = _DTYPES.get(t.dtype)
@@ -311,6 +319,8 @@ def _arg(t: torch.Tensor, what: str, rows: int, cols: int, device) -> tuple:
 
 
 def _vector(t: torch.Tensor, what: str, n: int, device) -> tuple:
+    if t.requires_grad:
+        _recorded(what)
     _need(t.dtype in _DTYPES, f"{what} must be float32, bfloat16 or float16")
     _need(t.numel() == n and t.is_contiguous(), f"{what} must be contiguous, with {n} elements")
     _need(t.device == device, "every tensor must be on one device")

@@ -97,3 +97,44 @@ def test_packed_inputs_give_their_shape_to_the_output(monkeypatch):
                 assert pk.linear8(src, w, out=out).y is out
     by_hand = pk.Packed8(torch.zeros(15, 128, dtype=U8), torch.full((15, 4), 127, dtype=U8), 40)
     assert pk.linear8(by_hand, w).y.shape == (15, 24) and pk.unpack8(pk.pack8(torch.zeros(3, 5, 40))).shape == (15, 40)
+
+
+def needs_gradient(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16, requires_grad=True)
+
+
+@pytest.mark.parametrize("call", [
+    lambda x, w: pk.pack8(x(4, 6)), lambda x, w: pk.linear8(x(4, 6), w(8, 6)), lambda x, w: pk.gated8(x(4, 6), w(8, 6), w(8, 6)),
+    lambda x, w: pk.linear8(w(4, 6), w(8, 6), bias=x(8)), lambda x, w: pk.linear8(w(4, 6), w(8, 6), residual=x(4, 8)),
+    lambda x, w: pk.linear8_backward(x(4, 8), w(4, 8), activation="gelu"), lambda x, w: pk.gated8_backward(x(4, 8), w(4, 8), w(4, 8)),
+    lambda x, w: pk.weight_grad8(x(4, 8), w(4, 6)), lambda x, w: pk.input_grad8(x(4, 8), w(8, 6)),
+    lambda x, w: pk.unpack8(w(4, 6), out=x(4, 6)),
+])
+def test_inputs_that_require_a_gradient(call, monkeypatch):
+    """Nothing is recorded, so a result would be cut off from its input without a word: refused, but where nothing is to
+    be recorded."""
+    monkeypatch.setattr(layers, "_run", lambda *args: None)
+    packed = lambda r, c: pk.Packed8(torch.zeros(r, 128 * -(-c // 128), dtype=U8), torch.full((r, 4), 127, dtype=U8), c)  # noqa: E731
+    with pytest.raises(ValueError, match="requires a gradient"):
+        call(needs_gradient, packed)
+    with torch.no_grad():
+        call(needs_gradient, packed)
+    call(lambda *shape: needs_gradient(*shape).detach(), packed)
+
+
+def test_inside_a_function_of_autograd(monkeypatch):
+    """torch.autograd.Function runs its own forward and backward passes with nothing recorded."""
+    monkeypatch.setattr(layers, "_run", lambda *args: None)
+    w = pk.Packed8(torch.zeros(8, 128, dtype=U8), torch.full((8, 4), 127, dtype=U8), 6)
+
+    class Layer(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return pk.linear8(x, w).y
+
+        @staticmethod
+        def backward(ctx, dy):
+            return pk.input_grad8(dy, w)
+    x = needs_gradient(4, 6)
+    Layer.apply(x).square().sum().backward()
+    assert x.grad.shape == x.shape
