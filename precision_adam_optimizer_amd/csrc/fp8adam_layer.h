@@ -22,7 +22,6 @@ using fp8adam_list::vu2_any;
 using fp8adam_list::vu4_any;
 
 typedef float vf4_t __attribute__((ext_vector_type(4)));
-typedef float vf16_t __attribute__((ext_vector_type(16)));
 
 // ------------------------------------------------------------------- typed rows
 
@@ -110,7 +109,8 @@ __device__ __forceinline__ void st8(int dt, void* base, int64_t i, int64_t n, co
 // ------------------------------------------------------------------ activations
 
 // e^x from the hardware's 2^x, with the rounding of x * log2 e put right to first order: within
-// 2 ulp.  Out of its range it is 0 or Inf (and without the correction, which would be Inf * 0).
+// 2 ulp for |x| < 87.3 (2^126).  Beyond that it is 0, Inf or, without the correction, which would be Inf * 0, within
+// 2^-17: sigmoid(z) and e^(-z^2/2) are below the normal numbers there, or 1 is added.
 __device__ __forceinline__ float exp_of(float x) {
   constexpr float kL = 1.44269502f, kLlo = 1.92596303e-8f, kLn2 = 0.693147182f;  // log2 e in two parts
   const float t = x * kL;

@@ -106,8 +106,9 @@ constexpr int kActRows = 64;  // of a work-group
 
 // One block of 128 columns of kActRows rows, eight columns per lane: reads and writes at once, bound
 // by HBM (4096 x 11008 gated in bf16: 71 us, 5.0 TB/s).  Each row is loaded when the one before has
-// been written; all four loaded first took 77 us (twice the registers, half the waves).  The sums over the rows, for the bias, are added up in fp32 by each lane and then over
-// the work-group's 16 rows of lanes, always in the same order; k_bias_join adds the chunks.
+// been written; all four loaded first took 77 us (twice the registers, half the waves).  The sums over
+// the rows, for the bias, are added up in fp32 by each lane and then over the work-group's 16 rows of
+// lanes, always in the same order; k_bias_join adds the chunks.
 template <bool GATED, int ACT, int DT>
 __global__ __launch_bounds__(kThreads) void k_act_backward(const ActArgs a) {
   const int64_t chunk = blockIdx.x / a.nb;
@@ -629,11 +630,11 @@ auto guarded(const char* what, F&& body) -> decltype(body()) {
 // The tiles and the number of parts of the sum whose estimated time is least, in us: 64 of the sum
 // take a work-group of 256 x 256 (one on a CU) 2, one of 128 x 128 1, or 1.35 where there are two on
 // a CU; the parts are written and read again at about 5 TB/s, by one launch more.  (The estimates are
-// within 15% of what was measured, and their order right: 2048 x 2048 x 2048 as 128 x 128 in one
+// within a sixth of what was measured, and their order right: 2048 x 2048 x 2048 as 128 x 128 in one
 // part 45 estimated 38, as 256 x 256 in four parts 51 estimated 53; 2048 tokens x 2 pairs of 2048 x 768
 // as 128 x 128 in five parts 35 estimated 40, as 256 x 256 in eight 40 estimated 46; 16384 tokens
-// x 2048 x 768 as 256 x 256 in ten parts 80 estimated 87, as 128 x 128 in five 88 estimated 93.)  Of large
-// numbers of parts one in eight is looked at: all 768 of a single tile would take the host longer than the kernel's launch.
+// x 2048 x 768 as 256 x 256 in ten parts 80 estimated 87, as 128 x 128 in five 88 estimated 93.)  From 16 on the numbers
+// of parts that are looked at grow by an eighth: all 768 of a single tile would take the host longer than the kernel's launch.
 GradPlan plan_grad(int64_t m, int64_t k, int64_t r, int npairs) {
   const int64_t steps = (r + 63) / 64 * npairs, ldp = (k + 3) & ~(int64_t)3;
   GradPlan best{0, 1, 0};

@@ -40,7 +40,7 @@ __device__ __forceinline__ v8bf tr_frag(const uint8_t* tile, uint32_t off) {
   return __builtin_bit_cast(v8bf, v8s{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
 }
 
-// Sixteen codes times their scale, in bf16 (exact: a code has at most four significant bits).
+// Sixteen codes times their scale, in bf16 (exact, a code has at most four significant bits, but for what lies below 2^-133).
 template <int BF>
 __device__ __forceinline__ void widen(const vu4& c, float s, vu4 (&out)[2]) {
 #pragma unroll
@@ -331,8 +331,7 @@ __global__ __launch_bounds__(128 * WK, 2) void k_grad(const GradArgs a, int spli
 }
 
 // out (+)= the sum of the parts, in their order.
-template <int DUMMY>
-__global__ __launch_bounds__(kThreads) void k_grad_join(const GradArgs a, int splits) {
+static __global__ __launch_bounds__(kThreads) void k_grad_join(const GradArgs a, int splits) {
   const int64_t ldp = ((int64_t)a.k + 3) & ~(int64_t)3, groups = ldp >> 2;
   const int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (q >= a.m * groups) return;
@@ -361,7 +360,7 @@ int launch_grad_tile(const GradArgs& a, const GradPlan& p, hipStream_t s) {
                   : launch(k_grad<false, BF, MT, KT, WK>, grid, block, 0, s, a, p.splits, (int)tm, (int)tk);
   if (r || p.splits == 1) return r;
   const int64_t threads = a.m * (((int64_t)a.k + 3) >> 2);
-  return launch(k_grad_join<0>, dim3((unsigned)((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, a, p.splits);
+  return launch(k_grad_join, dim3((unsigned)((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, a, p.splits);
 }
 
 template <int BF>

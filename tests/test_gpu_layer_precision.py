@@ -92,3 +92,55 @@ def test_gradients_of_one_token_are_rounded_once():
     x = pk.pack8(u.randn((1, 500), 2))
     want = dy.double().t() @ u.values(x)
     assert ((pk.weight_grad8(dy, x).double() - want).abs() <= 3 * 2.0 ** -24 * want.abs()).all()  # three terms are added
+
+
+def activations(rows, cols, seed, columns_that_stand_out):
+    """Normal numbers; or rows of different sizes and a hundredth of the columns eight times as large."""
+    x = u.randn((rows, cols), seed, spread=0.5 if columns_that_stand_out else 0.0)
+    if columns_that_stand_out:
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        x = x * torch.where(torch.rand(cols, generator=g, device="cuda") < 0.01, 8.0, 1.0)
+    return x
+
+
+@pytest.mark.parametrize("stand_out, typical", [(False, 1.4e-5), (True, 2.7e-5)])
+@pytest.mark.parametrize("tokens, cols, rows", [(2048, 768, 2048), (1027, 1000, 2050), (1024, 4096, 2048)])
+def test_what_the_fp8_instruction_cuts(tokens, cols, rows, stand_out, typical):
+    """The figures that the header gives, within a factor of 1.5: the error of the sums next to their rms, read off
+    what is left beside a residual that takes the sums away, and the kept codes on the other side of a border."""
+    x, w = pk.pack8(activations(tokens, cols, 1, stand_out)), pk.pack8(u.randn((rows, cols), 2) / cols ** 0.5)
+    z = u.values(x) @ u.values(w).t()
+    codes = u.pack(z.float(), "e4m3")[0]
+    for exact, most, share in ((False, 1.5 * typical, 1.5 / 640), (True, 2e-7, 1.5 / 190000)):
+        r = pk.linear8(x, w, residual=-z.float(), keep="e4m3", exact=exact)  # (the residual's own rounding: 2^-24)
+        error = (r.y.double().square().mean() / z.square().mean()).sqrt().item()
+        differ = (r.z.codes[:, :rows] != codes[:, :rows]).double().mean().item()
+        print(f"exact {exact}: error {error:.3g} of the rms, kept codes that differ 1 in {1 / differ if differ else 0:.0f}")
+        assert error <= most
+        assert differ <= share
+        if not exact:
+            assert error >= typical / 1.5 and differ >= 1 / (1.5 * 990)
+
+
+@pytest.mark.parametrize("fmt, first", [("e4m3", 3), ("e5m2", 10)])
+def test_smallest_scales(fmt, first):
+    """Every code under the smallest scales, times a power of two: exact from the scale on whose smallest code is 2^-133, and
+    below it off by half of that at most."""
+    n = 126 if fmt == "e4m3" else 123
+    codes = torch.zeros(n, 128, dtype=torch.uint8, device="cuda")
+    codes[:, 0] = torch.arange(1, n + 1, device="cuda")
+    big = 2.0 ** 100
+    w = pk.pack8(torch.full((1, 128), big, device="cuda"))
+    dy = torch.full((1, 1), big, dtype=BF16, device="cuda")
+    for byte in (1, 2, 3, 5, 8, 9, 10, 11, 30):
+        scales = torch.full((n, 4), byte, dtype=torch.uint8, device="cuda")
+        x = pk.Packed8(codes, scales, 128, fmt)
+        want = u.values(x)[:, 0]
+        off = 0.0 if byte >= first else 2.0 ** -134
+        assert torch.equal(pk.unpack8(x, F32).double()[:, 0], want)
+        few = torch.cat([pk.linear8(pk.Packed8(codes[i:i + 50], scales[i:i + 50], 128, fmt), w, dtype=F32).y for i in range(0, n, 50)])
+        tile = pk.linear8(x, w, dtype=F32).y  # more than 64 tokens
+        grad = torch.cat([pk.weight_grad8(dy, pk.Packed8(codes[i:i + 1], scales[i:i + 1], 128, fmt))[:, :1] for i in range(n)])
+        for got in (few, tile, grad):
+            assert ((got.double()[:, 0] / big - want).abs() <= off).all(), byte
