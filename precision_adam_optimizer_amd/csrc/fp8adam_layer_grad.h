@@ -75,9 +75,9 @@ __device__ __forceinline__ void widen(const vu4& c, float s, vu4 (&out)[2]) {
 // The sums then go through shared memory into whole rows of the tile, so that whole lines are
 // read (accumulate) and written.
 //
-// Measured: 4096 tokens x 11008 x 4096 added to fp32 in 437 us (843 TFLOP/s; the gradient's 360 MB alone
-// take 61), the input's gradient of two such layers in 682 (1080; the library's product of bf16 by bf16
-// reaches 1224 of 8192^3).  There the matrix cores are busy 44% of the time and shared memory's reads 31%
+// Measured: 4096 tokens x 11008 x 4096 added to fp32 in 434 us (850 TFLOP/s; the gradient's 360 MB alone
+// take 61), the input's gradient of two such layers in 673 (1100; the library's product of bf16 by bf16
+// reaches 1224 of 8192^3); of fp32 gradients, three terms each, in 1148 and 1978.  There the matrix cores are busy 45% of the time and shared memory's reads 31%
 // (a fifth of that conflicts of the transposing ones): a turn takes about 1040 cycles, of which its
 // products need 512 and the other waves' 64 KB of reads as many, behind the issue of the loads and
 // before the barrier.  Blocks of 32 in two buffers took 669 us, and in four with half lines 740.

@@ -16,7 +16,7 @@
 // counts, whether or not something is kept, and where the caller asks for it, both operands are widened to
 // bf16 times their scales, which is exact (but for what lies below 2^-133, under scales below 2^-124
 // of E4M3 and 2^-117 of E5M2), and multiplied by the bf16 instruction, which adds every product in 32
-// bits (4096 tokens x 4096 x 2 * 11008, both kept: 620 us in place of 320; 2048 x 768 x 2 * 2048: 3 us more).
+// bits (4096 tokens x 4096 x 2 * 11008, both kept: 630 us in place of 329; 2048 x 768 x 2 * 2048: 21 and 17).
 //
 // The order of the products in one instruction is free, so a lane may take any 32 columns of
 // its row as long as both operands take the same: here two of a row's 16-byte pieces.
