@@ -144,3 +144,64 @@ def test_smallest_scales(fmt, first):
         grad = torch.cat([pk.weight_grad8(dy, pk.Packed8(codes[i:i + 1], scales[i:i + 1], 128, fmt))[:, :1] for i in range(n)])
         for got in (few, tile, grad):
             assert ((got.double()[:, 0] / big - want).abs() <= off).all(), byte
+
+
+def exact_step(x, w, dy, out):
+    """Forward with every product in fp32, kept, and both gradients of an fp32 dy."""
+    r = pk.linear8(x, w, activation="silu", keep="e4m3", exact=True)
+    dz = pk.linear8_backward(dy, r.z, activation="silu")
+    return [r.y, r.z.codes, dz, pk.weight_grad8(dz, r.x, out, accumulate=True), pk.input_grad8([dz, dy], [w, w], dtype=F32)]
+
+
+def test_exact_calls_captured_and_on_two_streams():
+    """Two graphs, whose workspaces are their own, replayed in turn with eager work between; then the calls on two streams at
+    once: the same bits as alone."""
+    w = pk.pack8(u.randn((520, 256), 1) / 16)
+    graphs = []
+    for tokens in (40, 900):
+        x, dy, out = (torch.zeros(s, dtype=d, device="cuda") for s, d in (((tokens, 256), BF16), ((tokens, 520), F32), ((520, 256), F32)))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            exact_step(x, w, dy, out)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = exact_step(x, w, dy, out)
+        graphs.append((g, x, dy, out, outs))
+    for r in range(4):
+        for g, x, dy, out, outs in graphs:
+            x.copy_(u.randn(x.shape, 10 + r, dtype=BF16))
+            dy.copy_(u.randn(dy.shape, 20 + r))
+            out.zero_()
+            g.replay()
+            want = exact_step(x.clone(), w, dy.clone(), torch.zeros_like(out))
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs, want)), r
+    args = [(x.clone(), w, dy.clone()) for _, x, dy, _, _ in graphs]
+    want = [exact_step(*a, torch.zeros(520, 256, device="cuda")) for a in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for s, a in zip(streams, args):
+            with torch.cuda.stream(s):
+                got.append(exact_step(*a, torch.zeros(520, 256, device="cuda")))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for v, x in zip(got, want) for a, b in zip(v, x))
+
+
+def test_parts_of_a_gradient_past_32_bits():
+    """An fp32 gradient whose parts are more than 2^32 bytes each: the sums of its last rows."""
+    tokens, rows, cols = 1_100_000, 2056, 100
+    dy = torch.zeros(tokens, rows, device="cuda")
+    dy[-500:] = u.randn((500, rows), 1)
+    x = pk.pack8(torch.ones(tokens, cols, device="cuda") * 0.5)
+    d = dy[-500:].double()
+    want = (d.t() @ torch.full((500, cols), 0.5, dtype=torch.float64, device="cuda"))
+    assert ((pk.weight_grad8(dy, x).double() - want).abs() <= u.sum_bound(0.5 * d.abs().sum(0)[:, None], 3 * 500 + 300)).all()
+    w = pk.pack8(u.randn((rows, cols), 2) / 45)
+    dx = pk.input_grad8(dy, w, dtype=F32)
+    wv = u.values(w)
+    assert not dx[:-500].any()
+    assert ((dx[-500:].double() - d @ wv).abs() <= u.sum_bound(d.abs() @ wv.abs(), 3 * rows + 300)).all()
